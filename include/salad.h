@@ -17,7 +17,8 @@
  * Conventions shared by every entry point
  *   - Tensors Q, K, V, O are bf16, contiguous, [B, H, N, d] with the exact
  *     token count N (no caller padding).  d must be 64 or 128; the block
- *     size must be 64.  N must be in [1, 262144].
+ *     size must be 64.  N must be in [1, 262144].  (salad_rope takes other types,
+ *     sizes and strides too; see there.)
  *   - All tensor pointers are DEVICE pointers, 16-byte aligned, owned by the
  *     caller.  Pointers documented as HOST are read during the call only.
  *   - The library never allocates or frees device memory and never
@@ -305,6 +306,62 @@ typedef struct salad_forward_args {
 
 size_t salad_forward_workspace_bytes(const salad_forward_args* args);
 salad_status salad_forward(const salad_forward_args* args, salad_stream stream);
+
+/*
+ * Rotary positions with several axes (time, height, width) on queries and
+ * keys, and the backward pass.  Every channel pair of a token turns by
+ * angle = position[axis] * rate:
+ *   y_u = x_u cos(angle) - x_w sin(angle),  y_w = x_u sin(angle) + x_w cos(angle).
+ * The d channels belong to three axes, split[0] + split[1] + split[2] = d
+ * (each even and >= 0; an unused axis has 0): pair i of a group of g channels
+ * turns at rate base^(-2i/g).  This is the encoding that salad_forward's
+ * rope3d option applies inside the linear branch ("SALAD ...
+ * (paper.rainbus.top)" 方法步骤详情 step 3), for the tensors that enter the
+ * sparse branch or a cache, with any split, on any axes.
+ *   pairing SALAD_PAIR_ADJACENT: pair m is channels (2m, 2m + 1);
+ *           SALAD_PAIR_HALVES:   pair m is channels (m, m + d/2).
+ *   The first split[0]/2 pairs are axis 0's, then axis 1's, then axis 2's.
+ * Positions: `positions`, or, where it is NULL, the latent grid: token n of
+ * every sample stands at p = offset + n, position (p / (Hh Wh), p / Wh % Hh,
+ * p % Wh) (frame-major).
+ * inverse = 1 turns by -angle: the backward pass, since dx = R^T dy.
+ * Angles are formed and reduced in float64, products are float32, and the
+ * result is rounded once to the tensors' type.
+ * Layout: rows of d contiguous elements; strides in elements of the batch,
+ * head and token dimensions (multiples of 16 bytes; 0 in an input where it
+ * is broadcast).  q_out may be q itself (same pointer and strides), likewise
+ * k_out and k; outputs otherwise overlap no input, nor each other.  q and k
+ * may be interleaved slices of one buffer.
+ * d: a multiple of 16 from 16 to 256.  Needs no workspace.
+ */
+#define SALAD_BF16 0
+#define SALAD_F16  1
+#define SALAD_F32  2
+#define SALAD_PAIR_ADJACENT 0
+#define SALAD_PAIR_HALVES   1
+
+typedef struct salad_strides {
+    int64_t b, h, n;            /* elements between samples, heads, tokens */
+} salad_strides;
+
+typedef struct salad_rope_args {
+    const void* q;              /* [B,Hq,N,d] device */
+    void* q_out;                /* [B,Hq,N,d] device (out) */
+    const void* k;              /* [B,Hk,N,d] device, or NULL with Hk = 0 */
+    void* k_out;                /* [B,Hk,N,d] device (out), or NULL */
+    salad_strides q_st, qo_st, k_st, ko_st;
+    int dtype;                  /* SALAD_BF16, SALAD_F16 or SALAD_F32, of all four tensors */
+    int B, Hq, Hk, N, d;
+    const int32_t* positions;   /* device [N,3], or [B,N,3] with positions_batched = 1; or NULL */
+    int positions_batched;
+    int Hh, Wh, offset;         /* the grid, where positions is NULL; offset >= 0 */
+    int split[3];
+    float base;                 /* > 1 */
+    int pairing;
+    int inverse;
+} salad_rope_args;
+
+salad_status salad_rope(const salad_rope_args* args, salad_stream stream);
 
 /*
  * Reads and clears the device-side error word after synchronising `stream`.

@@ -17,7 +17,7 @@ import torch
 __all__ = [
     "SaladError", "lib", "status_string", "version",
     "gate", "gate_noalloc", "select_blocks", "linear_state", "linear_apply", "permute_tokens",
-    "project",
+    "project", "rope", "rope_backward",
     "sparse_attn", "dense_attn", "forward", "ForwardPlan", "forward_workspace_bytes",
     "check_error", "debug_wait_timeout",
     "MODE_TOPK", "MODE_SWA", "MODE_DENSE", "EXPORTED_SYMBOLS",
@@ -39,7 +39,7 @@ EXPORTED_SYMBOLS = (
     "salad_sparse_attn_workspace_bytes", "salad_sparse_attn", "salad_dense_attn",
     "salad_forward_workspace_bytes", "salad_forward",
     "salad_check_error", "salad_debug_wait_timeout",
-    "salad_gate_noalloc", "salad_project",
+    "salad_gate_noalloc", "salad_project", "salad_rope",
 )
 
 
@@ -73,6 +73,27 @@ class ForwardArgs(ctypes.Structure):
     ]
 
 
+class Strides(ctypes.Structure):
+    """Mirror of salad_strides (elements between samples, heads, tokens)."""
+    _fields_ = [("b", ctypes.c_int64), ("h", ctypes.c_int64), ("n", ctypes.c_int64)]
+
+
+class RopeArgs(ctypes.Structure):
+    """Mirror of salad_rope_args."""
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+        ("k", ctypes.c_void_p), ("k_out", ctypes.c_void_p),
+        ("q_st", Strides), ("qo_st", Strides), ("k_st", Strides), ("ko_st", Strides),
+        ("dtype", ctypes.c_int),
+        ("B", ctypes.c_int), ("Hq", ctypes.c_int), ("Hk", ctypes.c_int), ("N", ctypes.c_int),
+        ("d", ctypes.c_int),
+        ("positions", ctypes.c_void_p), ("positions_batched", ctypes.c_int),
+        ("Hh", ctypes.c_int), ("Wh", ctypes.c_int), ("offset", ctypes.c_int),
+        ("split", ctypes.c_int * 3), ("base", ctypes.c_float),
+        ("pairing", ctypes.c_int), ("inverse", ctypes.c_int),
+    ]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libsalad.so not built ({LIB_PATH}); run "
@@ -100,6 +121,7 @@ def _load() -> ctypes.CDLL:
         "salad_check_error": (i, [vp]),
         "salad_debug_wait_timeout": (i, [ctypes.c_ulonglong, vp]),
         "salad_gate_noalloc": (i, [vp, vp, f, i, i, i, vp, vp]),
+        "salad_rope": (i, [ctypes.POINTER(RopeArgs), vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -188,6 +210,22 @@ def _workspace(nbytes: int, device, workspace: Optional[torch.Tensor]) -> Option
             raise ValueError("workspace too small")
         return workspace
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _dev_rows(t, dtype, name: str) -> Strides:
+    """A [B, H, N, d] tensor with contiguous rows of d and any other strides,
+    on the current device; returns its strides."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    b, h, n, c = t.stride()
+    if c != 1:
+        raise ValueError(f"{name} must have contiguous rows (the last dimension's stride is {c})")
+    return Strides(b, h, n)
 
 
 def _flags(space_major_heads, H: int):
@@ -330,6 +368,104 @@ def project(a: torch.Tensor, w: torch.Tensor, *, out_per_head: bool = False, res
                              _ptr(resid), _ptr(s), float(drop_threshold), _stream(stream)),
            "salad_project")
     return out
+
+
+def _empty_on(stream, make):
+    """``make()``'s new tensor, allocated on the stream that the call runs on:
+    memory of another stream could still be in use there, or be handed out
+    again while this call uses it."""
+    if stream is None:
+        return make()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(stream):
+        return make()
+
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_PAIRINGS = {"adjacent": 0, "halves": 1}
+_NO_STRIDES = Strides(0, 0, 0)
+
+
+def _rotation(d: int, split, pairing: str, positions, grid, B: int, N: int):
+    """(split, pairing, batched, Hh, Wh) of a rotation, checked."""
+    if split is None:
+        dy = 2 * (d // 6)
+        split = (d - 2 * dy, dy, dy)
+    if len(split) != 3:
+        raise ValueError("split must name the channels of three axes")
+    if pairing not in _PAIRINGS:
+        raise ValueError(f"pairing must be one of {sorted(_PAIRINGS)}")
+    if (positions is None) == (grid is None):
+        raise ValueError("give the tokens' positions or their grid")
+    batched, Hh, Wh = 0, 0, 0
+    if positions is not None:
+        _dev_tensor(positions, torch.int32, "positions")
+        batched = int(positions.dim() == 3)
+        _shape(positions, (B, N, 3) if batched else (N, 3), "positions")
+    else:
+        Hh, Wh = grid
+    return tuple(int(c) for c in split), _PAIRINGS[pairing], batched, int(Hh), int(Wh)
+
+
+def _rope(what: str, q, k, positions, grid, offset, base, split, pairing, inverse, q_out, k_out,
+          stream):
+    _dims(q, 4, "q", "[B, H, N, d]")
+    B, Hq, N, d = q.shape
+    if q.dtype not in _DTYPES:
+        raise ValueError(f"q must be bfloat16, float16 or float32, got {q.dtype}")
+    if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
+        raise ValueError(f"{what} is not recorded by autograd: call it under torch.no_grad() and "
+                         "turn the gradients with rope_backward")
+    if q_out is not None:
+        _shape(q_out, q.shape, "q_out")
+    q_st = _dev_rows(q, q.dtype, "q")
+    q_out = _empty_on(stream, lambda: torch.empty_like(q)) if q_out is None else q_out
+    qo_st = _dev_rows(q_out, q.dtype, "q_out")
+    Hk, k_st, ko_st = 0, _NO_STRIDES, _NO_STRIDES
+    if k is not None:
+        _dims(k, 4, "k", "[B, H, N, d]")
+        Hk = k.shape[1]
+        _shape(k, (B, Hk, N, d), "k")
+        if k_out is not None:
+            _shape(k_out, k.shape, "k_out")
+        k_st = _dev_rows(k, q.dtype, "k")
+        k_out = _empty_on(stream, lambda: torch.empty_like(k)) if k_out is None else k_out
+        ko_st = _dev_rows(k_out, q.dtype, "k_out")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    split, pair, batched, Hh, Wh = _rotation(d, split, pairing, positions, grid, B, N)
+    a = RopeArgs(_ptr(q), _ptr(q_out), _ptr(k), _ptr(k_out), q_st, qo_st, k_st, ko_st,
+                 _DTYPES[q.dtype], B, Hq, Hk, N, d, _ptr(positions), batched, Hh, Wh, int(offset),
+                 split, float(base), pair, inverse)
+    _check(lib.salad_rope(ctypes.byref(a), _stream(stream)), what)
+    return q_out if k is None else (q_out, k_out)
+
+
+def rope(q: torch.Tensor, k: Optional[torch.Tensor] = None, *, positions=None, grid=None,
+         offset: int = 0, base: float = 10000.0, split: Optional[Sequence[int]] = None,
+         pairing: str = "adjacent", q_out=None, k_out=None, stream=None):
+    """Rotary positions with up to three axes on q [B,Hq,N,d] and k [B,Hk,N,d]
+    (bf16, fp16 or fp32; contiguous rows, any other strides): y = R(pos) x.
+
+    positions: int32 [N,3] or [B,N,3]; or grid = (Hh, Wh), the frame-major
+    latent whose token n stands at p = offset + n.  split: channels of the
+    three axes (default: the split of the linear branch's encoding,
+    d - 4*floor(d/6), 2*floor(d/6), 2*floor(d/6)).  pairing: "adjacent"
+    channels or "halves" of the row.  q_out, k_out: where to write (q and k
+    themselves turn in place).  Returns q_out, or (q_out, k_out) with k.
+    """
+    return _rope("salad_rope", q, k, positions, grid, offset, base, split, pairing, 0, q_out, k_out,
+                 stream)
+
+
+def rope_backward(dq: torch.Tensor, dk: Optional[torch.Tensor] = None, *, positions=None, grid=None,
+                  offset: int = 0, base: float = 10000.0, split: Optional[Sequence[int]] = None,
+                  pairing: str = "adjacent", q_out=None, k_out=None, stream=None):
+    """Gradients of rope()'s inputs from those of its outputs, dx = R(pos)^T dy;
+    arguments as for rope()."""
+    return _rope("salad_rope", dq, dk, positions, grid, offset, base, split, pairing, 1, q_out, k_out,
+                 stream)
 
 
 def permute_tokens(src: torch.Tensor, F: int, Hh: int, Wh: int, *, inverse: bool = False,

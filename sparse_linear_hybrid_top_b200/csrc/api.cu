@@ -5,6 +5,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <utility>
 
 #include "common.cuh"
 #include "internal.h"
@@ -745,6 +746,152 @@ salad_status salad_forward(const salad_forward_args* a, salad_stream stream) {
     if (launch_proj(c, p) != cudaSuccess) return SALAD_ERR_CUDA;
   }
   return SALAD_OK;
+}
+
+// ------------------------------------------------------------------ rope --
+namespace {
+
+// A strided [B, H, N, row] tensor's place in memory, in bytes.
+struct Strided {
+  const char* base;
+  long long size[3], stride[3];   // batch, head, token
+  long long row;
+  // Bytes from the first element to behind the last one, leaving dimension
+  // `but` out (-1: none).
+  long long extent(int but = -1) const {
+    long long e = row;
+    for (int i = 0; i < 3; ++i)
+      if (i != but) e += (size[i] - 1) * stride[i];
+    return e;
+  }
+};
+
+Strided strided(const void* base, const salad_strides& st, int B, int H, int N, long long row,
+                int elt) {
+  // The stride of a dimension of size 1 is never used, whatever it holds.
+  return Strided{static_cast<const char*>(base),
+                 {B, H, N},
+                 {B > 1 ? st.b * elt : 0, H > 1 ? st.h * elt : 0, N > 1 ? st.n * elt : 0},
+                 row};
+}
+
+// Strides that a kernel can use: rows on 16-byte boundaries, offsets within 62 bits.
+bool strides_ok(const Strided& t) {
+  for (int i = 0; i < 3; ++i)
+    if (t.stride[i] < 0 || t.stride[i] % 16 != 0 || t.stride[i] > (1ll << 42)) return false;
+  return aligned(t.base, 16);
+}
+
+// Whether every element has an address of its own (an output must).
+bool distinct(const Strided& t) {
+  int order[3] = {0, 1, 2};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if (t.stride[order[j]] < t.stride[order[i]]) std::swap(order[i], order[j]);
+  long long inner = t.row;
+  for (int i : order) {
+    if (t.size[i] == 1) continue;
+    if (t.stride[i] < inner) return false;
+    inner += (t.size[i] - 1) * t.stride[i];
+  }
+  return true;
+}
+
+bool apart(const Strided& a, const Strided& b) {
+  return a.base + a.extent() <= b.base || b.base + b.extent() <= a.base;
+}
+
+// Whether two tensors share no element: apart, or slices of one buffer that
+// are laid side by side along a common outer dimension (its stride holds both
+// slices whole, as in [B, N, 3, H, d] or [B, 3, H, N, d]).
+bool disjoint(const Strided& a, const Strided& b) {
+  if (apart(a, b)) return true;
+  // `outer`: the dimensions a common stride walks over, the token dimension
+  // alone (then the batch must be whole multiples of it) or the batch.
+  for (int outer : {2, 0}) {
+    const long long s = a.stride[outer];
+    if (s <= 0 || s != b.stride[outer]) continue;
+    Strided x = a, y = b;
+    x.size[outer] = y.size[outer] = 1;
+    if (outer == 2) {
+      if ((a.size[0] > 1 && a.stride[0] % s != 0) || (b.size[0] > 1 && b.stride[0] % s != 0)) continue;
+      x.size[0] = y.size[0] = 1;
+    }
+    long long delta = (b.base - a.base) % s;
+    if (delta < 0) delta += s;
+    if (delta >= x.extent() && delta + y.extent() <= s) return true;
+  }
+  return false;
+}
+
+bool same_place(const Strided& a, const Strided& b) {
+  if (a.base != b.base) return false;
+  for (int i = 0; i < 3; ++i)
+    if (a.size[i] > 1 && a.stride[i] != b.stride[i]) return false;
+  return true;
+}
+
+salad_status check_rotation(const int32_t* positions, int batched, int Hh, int Wh,
+                            const int (&split)[3], int d, float base, int pairing) {
+  if (split[0] < 0 || split[1] < 0 || split[2] < 0 || split[0] > d || split[1] > d || split[2] > d ||
+      split[0] + split[1] + split[2] != d || split[0] % 2 || split[1] % 2 || split[2] % 2)
+    return SALAD_ERR_INVALID_ARG;
+  if (!(base > 1.0f) || !std::isfinite(base)) return SALAD_ERR_INVALID_ARG;
+  if (pairing != SALAD_PAIR_ADJACENT && pairing != SALAD_PAIR_HALVES) return SALAD_ERR_INVALID_ARG;
+  if (batched != 0 && batched != 1) return SALAD_ERR_INVALID_ARG;
+  if (positions != nullptr) return aligned(positions, 4) ? SALAD_OK : SALAD_ERR_INVALID_ARG;
+  if (Hh < 1 || Wh < 1 || static_cast<long long>(Hh) * Wh > 0x7fffffffll) return SALAD_ERR_INVALID_ARG;
+  return SALAD_OK;
+}
+
+}  // namespace
+
+salad_status salad_rope(const salad_rope_args* a, salad_stream stream) {
+  if (a == nullptr) return SALAD_ERR_INVALID_ARG;
+  if (a->dtype != SALAD_BF16 && a->dtype != SALAD_F16 && a->dtype != SALAD_F32)
+    return SALAD_ERR_UNSUPPORTED;
+  if (a->B < 1 || a->B > 65535 || a->Hq < 1 || a->Hk < 0 || a->Hq > kMaxHeads || a->Hk > kMaxHeads ||
+      a->N < 1 || a->N > kMaxN)
+    return SALAD_ERR_INVALID_ARG;
+  if (a->d < 16 || a->d > 256 || a->d % 16 != 0) return SALAD_ERR_UNSUPPORTED;
+  if ((a->Hk > 0) != (a->k != nullptr) || (a->Hk > 0) != (a->k_out != nullptr))
+    return SALAD_ERR_INVALID_ARG;
+  salad_status st = check_rotation(a->positions, a->positions_batched, a->Hh, a->Wh, a->split, a->d,
+                                   a->base, a->pairing);
+  if (st != SALAD_OK) return st;
+  if (a->positions == nullptr && (a->offset < 0 || a->offset > 0x7fffffff - a->N))
+    return SALAD_ERR_INVALID_ARG;
+  if (a->inverse != 0 && a->inverse != 1) return SALAD_ERR_INVALID_ARG;
+  const int elt = a->dtype == SALAD_F32 ? 4 : 2;
+  const long long row = static_cast<long long>(a->d) * elt;
+  const Strided in[2] = {strided(a->q, a->q_st, a->B, a->Hq, a->N, row, elt),
+                         strided(a->k, a->k_st, a->B, a->Hk, a->N, row, elt)};
+  const Strided out[2] = {strided(a->q_out, a->qo_st, a->B, a->Hq, a->N, row, elt),
+                          strided(a->k_out, a->ko_st, a->B, a->Hk, a->N, row, elt)};
+  const int sides = a->Hk > 0 ? 2 : 1;
+  for (int i = 0; i < sides; ++i) {
+    if (!strides_ok(in[i]) || !strides_ok(out[i]) || !distinct(out[i])) return SALAD_ERR_INVALID_ARG;
+    if (!same_place(in[i], out[i]) && !disjoint(in[i], out[i])) return SALAD_ERR_INVALID_ARG;
+  }
+  if (sides == 2 && (!disjoint(out[0], out[1]) || !disjoint(out[0], in[1]) || !disjoint(out[1], in[0])))
+    return SALAD_ERR_INVALID_ARG;
+  Ctx c;
+  if ((st = get_ctx(stream, &c)) != SALAD_OK) return st;
+  RopeArgs r;
+  std::memset(&r, 0, sizeof(r));
+  auto put = [elt](long long (&to)[3], const Strided& s) {
+    for (int i = 0; i < 3; ++i) to[i] = s.stride[i] / elt;
+  };
+  r.q = a->q; r.q_out = a->q_out; r.k = a->k; r.k_out = a->k_out;
+  put(r.q_st, in[0]); put(r.qo_st, out[0]); put(r.k_st, in[1]); put(r.ko_st, out[1]);
+  r.dtype = a->dtype;
+  r.B = a->B; r.Hq = a->Hq; r.Hk = a->Hk; r.N = a->N; r.d = a->d;
+  r.where = RopeWhere{a->positions, a->positions_batched ? 3ll * a->N : 0ll, a->Hh, a->Wh, a->offset};
+  for (int i = 0; i < 3; ++i) r.split[i] = a->split[i];
+  r.base = a->base;
+  r.pairing = a->pairing;
+  r.inverse = a->inverse;
+  return from_cuda(launch_rope(c, r));
 }
 
 // ------------------------------------------------------------- errors --

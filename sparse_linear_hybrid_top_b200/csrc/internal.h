@@ -6,6 +6,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "rope.cuh"
+
 namespace salad {
 
 // Per-call launch context.
@@ -172,5 +174,25 @@ struct ProjArgs {
   float drop;
 };
 cudaError_t launch_proj(const Ctx& c, const ProjArgs& a);
+
+// ---- rotary positions (rope.cu)
+// y = x with every channel pair turned by position * rate (inverse: by the
+// negative angle).  Strides (batch, head, token) in elements; k may be null
+// with Hk = 0.
+struct RopeArgs {
+  const void* q;
+  void* q_out;
+  const void* k;
+  void* k_out;
+  long long q_st[3], qo_st[3], k_st[3], ko_st[3];
+  int dtype;                  // 0 bf16, 1 fp16, 2 fp32
+  int B, Hq, Hk, N, d;
+  RopeWhere where;
+  int split[3];
+  float base;
+  int pairing;                // 0 adjacent, 1 halves
+  int inverse;
+};
+cudaError_t launch_rope(const Ctx& c, const RopeArgs& a);
 
 }  // namespace salad
