@@ -17,8 +17,8 @@
  * Conventions shared by every entry point
  *   - Tensors Q, K, V, O are bf16, contiguous, [B, H, N, d] with the exact
  *     token count N (no caller padding).  d must be 64 or 128; the block
- *     size must be 64.  N must be in [1, 262144].  (salad_rope takes other types,
- *     sizes and strides too; see there.)
+ *     size must be 64.  N must be in [1, 262144].  (salad_rope takes other types
+ *     and sizes, and it and the cache operators take strides; see there.)
  *   - All tensor pointers are DEVICE pointers, 16-byte aligned, owned by the
  *     caller.  Pointers documented as HOST are read during the call only.
  *   - The library never allocates or frees device memory and never
@@ -364,11 +364,122 @@ typedef struct salad_rope_args {
 salad_status salad_rope(const salad_rope_args* args, salad_stream stream);
 
 /*
+ * A block cache of keys and values in 8 bits, for video generated chunk by
+ * chunk (and for single tokens): tokens of a sequence are held in blocks of
+ * 64.  A full ("closed") block is an e4m3 page of a shared pool with one
+ * power-of-two scale for its keys and one for its values per head; the open
+ * block behind it is kept in bf16, so that nothing is rounded twice.
+ *   k_pages, v_pages  uint8 (e4m3 codes) [pages, H, 64, d]
+ *   k_scale, v_scale  float32 [pages, H]: 2^e with the smallest e >= -100
+ *                     for which every |x| <= 448 * 2^e; a value is
+ *                     code * scale.  A block and head with an infinity or a
+ *                     NaN gets a NaN scale and reads as NaN.
+ *   k_tail, v_tail    bf16 [B, 2, H, 64, d]: the open block of each
+ *                     sequence, in one of two slots
+ *   page_table        int32 [B, blocks]: page of block j of sequence b
+ *   seq               int32 [B, 2]: tokens held (>= 0), tail slot (0 or 1)
+ * All are device pointers, contiguous, the pages and tails 16-byte aligned.
+ * d is 64 or 128.  An appended chunk goes to the other tail slot when it
+ * closes the open block, so (seq, tail) still describe the cache as it was:
+ * a chunk may be appended again at the same seq (each denoising step of a
+ * chunk does) and is kept by taking seq_out for the next seq.
+ * Pages that a call writes must differ from one another and from the pages
+ * of blocks that are to be kept.
+ * Table entries that are read and lie outside [0, pages) are skipped on the
+ * device; lengths, slots and counts out of range are forced into it, and
+ * tokens that the table has no room for (it holds 64 * blocks, and the open
+ * block 63 more) are dropped.  salad_check_error then returns
+ * SALAD_ERR_INVALID_ARG.
+ */
+typedef struct salad_cache {
+    void* k_pages;
+    void* v_pages;
+    float* k_scale;
+    float* v_scale;
+    void* k_tail;
+    void* v_tail;
+    const int32_t* page_table;
+    int B, H, d;                /* H: key/value heads */
+    int pages, blocks;
+} salad_cache;
+
+/*
+ * Append: token i < counts[b] of sequence b becomes token seq[b].len + i of
+ * the cache.  Keys are turned by salad_rope's encoding on the way where
+ * `rotate` is 1 (float32 products, rounded to bf16 before they are held): the
+ * positions of the new tokens, or, where positions is NULL, the grid
+ * position of p = seq[b].len + i.  Values are not turned.
+ * k, v: bf16 [B,H,N,d] with strides as in salad_rope.  counts: int32 [B]
+ * device or NULL (N each); rows behind a count are not read.
+ * seq_out: int32 [B,2], seq after the append; may be seq itself (a second,
+ * small launch advances it then) and may be NULL.
+ */
+typedef struct salad_cache_append_args {
+    salad_cache cache;
+    const int32_t* seq;
+    int32_t* seq_out;
+    const void* k;
+    const void* v;
+    salad_strides k_st, v_st;
+    int N;
+    const int32_t* counts;
+    int rotate;
+    const int32_t* positions;   /* device [N,3], or [B,N,3] with positions_batched = 1; or NULL */
+    int positions_batched;
+    int Hh, Wh;
+    int split[3];
+    float base;
+    int pairing;
+} salad_cache_append_args;
+
+salad_status salad_cache_append(const salad_cache_append_args* args, salad_stream stream);
+
+/*
+ * Attention over the cache: o = softmax(scale q k^T + M) v, the queries being
+ * the last counts[b] tokens that sequence b holds (append them first):
+ * query i < counts[b] stands at p = seq[b].len - counts[b] + i.
+ *   frame = F > 0: tokens come in groups of F (a latent frame; 1: one token).
+ *                  A query sees its own group, as far as it is held, and
+ *                  what is before it: keys j < min(len, (floor(p / F) + 1) F).
+ *   frame = 0:     every query sees all held keys.
+ *   window >= 0:   of the keys before the query's group (before the first
+ *                  query, for frame = 0) only the last `window` are seen;
+ *                  window < 0: all of them.
+ * A row that sees no key (an empty sequence, or p < 0) is 0 with lse = -inf.
+ * q, o: bf16 [B,Hq,N,d], strides as in salad_rope; Hq a multiple of the
+ * cache's H, query head h reading key/value head h / (Hq / H).  lse (may be
+ * NULL): float32 [B,Hq,N] contiguous, natural log of the sum of exponentials.
+ * Rows behind a count are left as they are.  o must not overlap q.
+ * Closed blocks are read as their exact values (code * scale); softmax
+ * statistics and sums are float32, P is rounded to bf16 for the product with
+ * the values.  Workspace: salad_cache_attn_workspace_bytes(args); two calls
+ * that may overlap on the GPU need two workspaces.
+ */
+typedef struct salad_cache_attn_args {
+    salad_cache cache;
+    const int32_t* seq;
+    const void* q;
+    void* o;
+    salad_strides q_st, o_st;
+    float* lse;
+    int Hq, N;
+    const int32_t* counts;
+    int frame, window;
+    float scale;                /* > 0, usually 1/sqrt(d) */
+    void* workspace;
+    size_t workspace_bytes;
+} salad_cache_attn_args;
+
+size_t salad_cache_attn_workspace_bytes(const salad_cache_attn_args* args);
+salad_status salad_cache_attn(const salad_cache_attn_args* args, salad_stream stream);
+
+/*
  * Reads and clears the device-side error word after synchronising `stream`.
  * Returns SALAD_ERR_TIMEOUT if any kernel gave up a bounded wait since the
  * last check; SALAD_ERR_CUDA if the stream reports an error or a kernel
  * refused to run (the attention kernel does when its dynamic shared memory
- * is not 1024-byte aligned); else SALAD_OK.
+ * is not 1024-byte aligned); SALAD_ERR_INVALID_ARG if a cache operator met
+ * a page, length, slot or count out of range; else SALAD_OK.
  */
 salad_status salad_check_error(salad_stream stream);
 

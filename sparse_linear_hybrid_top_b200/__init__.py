@@ -17,7 +17,7 @@ import torch
 __all__ = [
     "SaladError", "lib", "status_string", "version",
     "gate", "gate_noalloc", "select_blocks", "linear_state", "linear_apply", "permute_tokens",
-    "project", "rope", "rope_backward",
+    "project", "rope", "rope_backward", "BlockCache", "cache_append", "cache_attn",
     "sparse_attn", "dense_attn", "forward", "ForwardPlan", "forward_workspace_bytes",
     "check_error", "debug_wait_timeout",
     "MODE_TOPK", "MODE_SWA", "MODE_DENSE", "EXPORTED_SYMBOLS",
@@ -39,7 +39,8 @@ EXPORTED_SYMBOLS = (
     "salad_sparse_attn_workspace_bytes", "salad_sparse_attn", "salad_dense_attn",
     "salad_forward_workspace_bytes", "salad_forward",
     "salad_check_error", "salad_debug_wait_timeout",
-    "salad_gate_noalloc", "salad_project", "salad_rope",
+    "salad_gate_noalloc", "salad_project", "salad_rope", "salad_cache_append",
+    "salad_cache_attn_workspace_bytes", "salad_cache_attn",
 )
 
 
@@ -94,6 +95,41 @@ class RopeArgs(ctypes.Structure):
     ]
 
 
+class Cache(ctypes.Structure):
+    """Mirror of salad_cache."""
+    _fields_ = [
+        ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+        ("k_tail", ctypes.c_void_p), ("v_tail", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p),
+        ("B", ctypes.c_int), ("H", ctypes.c_int), ("d", ctypes.c_int),
+        ("pages", ctypes.c_int), ("blocks", ctypes.c_int),
+    ]
+
+
+class CacheAppendArgs(ctypes.Structure):
+    """Mirror of salad_cache_append_args."""
+    _fields_ = [
+        ("cache", Cache), ("seq", ctypes.c_void_p), ("seq_out", ctypes.c_void_p),
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_st", Strides), ("v_st", Strides),
+        ("N", ctypes.c_int), ("counts", ctypes.c_void_p), ("rotate", ctypes.c_int),
+        ("positions", ctypes.c_void_p), ("positions_batched", ctypes.c_int),
+        ("Hh", ctypes.c_int), ("Wh", ctypes.c_int), ("split", ctypes.c_int * 3),
+        ("base", ctypes.c_float), ("pairing", ctypes.c_int),
+    ]
+
+
+class CacheAttnArgs(ctypes.Structure):
+    """Mirror of salad_cache_attn_args."""
+    _fields_ = [
+        ("cache", Cache), ("seq", ctypes.c_void_p), ("q", ctypes.c_void_p), ("o", ctypes.c_void_p),
+        ("q_st", Strides), ("o_st", Strides), ("lse", ctypes.c_void_p),
+        ("Hq", ctypes.c_int), ("N", ctypes.c_int), ("counts", ctypes.c_void_p),
+        ("frame", ctypes.c_int), ("window", ctypes.c_int), ("scale", ctypes.c_float),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libsalad.so not built ({LIB_PATH}); run "
@@ -122,6 +158,9 @@ def _load() -> ctypes.CDLL:
         "salad_debug_wait_timeout": (i, [ctypes.c_ulonglong, vp]),
         "salad_gate_noalloc": (i, [vp, vp, f, i, i, i, vp, vp]),
         "salad_rope": (i, [ctypes.POINTER(RopeArgs), vp]),
+        "salad_cache_append": (i, [ctypes.POINTER(CacheAppendArgs), vp]),
+        "salad_cache_attn_workspace_bytes": (sz, [ctypes.POINTER(CacheAttnArgs)]),
+        "salad_cache_attn": (i, [ctypes.POINTER(CacheAttnArgs), vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -466,6 +505,150 @@ def rope_backward(dq: torch.Tensor, dk: Optional[torch.Tensor] = None, *, positi
     arguments as for rope()."""
     return _rope("salad_rope", dq, dk, positions, grid, offset, base, split, pairing, 1, q_out, k_out,
                  stream)
+
+
+class BlockCache:
+    """Buffers of an 8-bit block cache (``salad_cache`` in include/salad.h).
+
+    k_pages, v_pages: float8_e4m3fn [pages, H, 64, d]; k_scale, v_scale:
+    float32 [pages, H]; k_tail, v_tail: bf16 [B, 2, H, 64, d]; page_table:
+    int32 [B, blocks].  The tensors are checked once, here, and used by every
+    call; their contents are the program's to set and move (page_table above
+    all).  ``allocate`` makes them.
+    """
+
+    BLOCK = 64
+
+    def __init__(self, k_pages, v_pages, k_scale, v_scale, k_tail, v_tail, page_table):
+        _dims(k_pages, 4, "k_pages", "[pages, H, 64, d]")
+        pages, H, block, d = k_pages.shape
+        _dims(page_table, 2, "page_table", "[B, blocks]")
+        B, blocks = page_table.shape
+        _shape(k_pages, (pages, H, self.BLOCK, d), "k_pages")
+        _shape(v_pages, k_pages.shape, "v_pages")
+        for n, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            _shape(t, (pages, H), n)
+        for n, t in (("k_tail", k_tail), ("v_tail", v_tail)):
+            _shape(t, (B, 2, H, self.BLOCK, d), n)
+        for n, t, dt in (("k_pages", k_pages, torch.float8_e4m3fn), ("v_pages", v_pages, torch.float8_e4m3fn),
+                         ("k_scale", k_scale, torch.float32), ("v_scale", v_scale, torch.float32),
+                         ("k_tail", k_tail, torch.bfloat16), ("v_tail", v_tail, torch.bfloat16),
+                         ("page_table", page_table, torch.int32)):
+            _dev_tensor(t, dt, n)
+        self.k_pages, self.v_pages, self.k_scale, self.v_scale = k_pages, v_pages, k_scale, v_scale
+        self.k_tail, self.v_tail, self.page_table = k_tail, v_tail, page_table
+        self.B, self.H, self.d, self.pages, self.blocks = B, H, d, pages, blocks
+        self.device = page_table.device
+        self.args = Cache(_ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(k_tail),
+                          _ptr(v_tail), _ptr(page_table), B, H, d, pages, blocks)
+
+    @classmethod
+    def allocate(cls, B: int, H: int, d: int, blocks: int, *, pages: Optional[int] = None,
+                 device="cuda") -> "BlockCache":
+        """Empty buffers for B sequences of up to 64 * blocks tokens (and an
+        open block).  pages: size of the shared pool (default B * blocks, the
+        page table then naming every page once, in order)."""
+        n = B * blocks if pages is None else pages
+        page = lambda: torch.zeros(n, H, cls.BLOCK, d, dtype=torch.uint8,  # noqa: E731
+                                   device=device).view(torch.float8_e4m3fn)
+        tail = lambda: torch.zeros(B, 2, H, cls.BLOCK, d, dtype=torch.bfloat16, device=device)  # noqa: E731
+        scale = lambda: torch.ones(n, H, dtype=torch.float32, device=device)  # noqa: E731
+        table = torch.arange(B * blocks, dtype=torch.int32, device=device).reshape(B, blocks)
+        if pages is not None:
+            table.fill_(-1)
+        return cls(page(), page(), scale(), scale(), tail(), tail(), table)
+
+    def new_seq(self) -> torch.Tensor:
+        """seq of empty sequences: int32 [B, 2], tokens held and tail slot."""
+        return torch.zeros(self.B, 2, dtype=torch.int32, device=self.device)
+
+
+def _cache_call(cache, seq, counts):
+    if not isinstance(cache, BlockCache):
+        raise ValueError("cache must be a BlockCache")
+    if cache.device.index != torch.cuda.current_device():
+        raise ValueError(f"cache is on {cache.device}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    _shape(seq, (cache.B, 2), "seq")
+    _dev_tensor(seq, torch.int32, "seq")
+    if counts is not None:
+        _shape(counts, (cache.B,), "counts")
+        _dev_tensor(counts, torch.int32, "counts")
+
+
+def cache_append(cache: BlockCache, k: torch.Tensor, v: torch.Tensor, seq: torch.Tensor, *,
+                 counts=None, positions=None, grid=None, base: float = 10000.0,
+                 split: Optional[Sequence[int]] = None, pairing: str = "adjacent", seq_out=None,
+                 stream=None) -> torch.Tensor:
+    """Appends k, v (bf16 [B,H,N,d], contiguous rows, any other strides) to the
+    cache behind the tokens that ``seq`` says it holds, and returns seq_out,
+    the state after it (``seq`` itself may be given: it is advanced in place).
+
+    counts: int32 [B], valid tokens of each row of the batch (default all N).
+    positions (int32 [N,3] or [B,N,3]) or grid = (Hh, Wh): turn the keys as
+    rope() does, at the given positions or at the cache position of each token
+    on the grid; neither: the keys are held as they come.  The cache as ``seq``
+    describes it is not changed, so a chunk can be appended again at the same
+    ``seq`` (pages of blocks behind it are overwritten).
+    """
+    _dims(k, 4, "k", "[B, H, N, d]")
+    _cache_call(cache, seq, counts)
+    N = k.shape[2]
+    _shape(k, (cache.B, cache.H, N, cache.d), "k")
+    _shape(v, k.shape, "v")
+    k_st, v_st = _dev_rows(k, torch.bfloat16, "k"), _dev_rows(v, torch.bfloat16, "v")
+    rotate = int(positions is not None or grid is not None)
+    if rotate:
+        split, pair, batched, Hh, Wh = _rotation(cache.d, split, pairing, positions, grid, cache.B, N)
+    else:
+        split, pair, batched, Hh, Wh = (0, 0, 0), 0, 0, 0, 0
+    if seq_out is None:
+        seq_out = _empty_on(stream, lambda: torch.empty_like(seq))
+    else:
+        _shape(seq_out, seq.shape, "seq_out")
+        _dev_tensor(seq_out, torch.int32, "seq_out")
+    a = CacheAppendArgs(cache.args, _ptr(seq), _ptr(seq_out), _ptr(k), _ptr(v), k_st, v_st, N,
+                        _ptr(counts), rotate, _ptr(positions), batched, Hh, Wh, split, float(base), pair)
+    _check(lib.salad_cache_append(ctypes.byref(a), _stream(stream)), "salad_cache_append")
+    return seq_out
+
+
+def cache_attn(cache: BlockCache, q: torch.Tensor, seq: torch.Tensor, *, counts=None, frame: int = 0,
+               window: int = -1, scale: Optional[float] = None, o=None, lse=None, workspace=None,
+               stream=None) -> torch.Tensor:
+    """Attention of q (bf16 [B,Hq,N,d], contiguous rows, any other strides),
+    the last tokens that ``seq`` says the cache holds, over the whole cache.
+
+    Hq is a multiple of the cache's heads.  counts: int32 [B], valid rows of
+    each sample (default all N; the others are not written).  frame: 0, every
+    query sees every key; F > 0, a query sees the tokens of its own group of F
+    tokens and those before it (1: causal by token).  window >= 0: of the keys
+    before the query's group only the last ``window``.  scale: of the scores
+    (default 1/sqrt(d)).  lse: float32 [B,Hq,N], filled with the natural log
+    of the sum of exponentials.  Rows that see no key are 0, with lse = -inf.
+    """
+    _dims(q, 4, "q", "[B, H, N, d]")
+    _cache_call(cache, seq, counts)
+    B, Hq, N, d = q.shape
+    _shape(q, (cache.B, Hq, N, cache.d), "q")
+    q_st = _dev_rows(q, torch.bfloat16, "q")
+    if o is None:
+        o = _empty_on(stream, lambda: torch.empty_like(q))
+    else:
+        _shape(o, q.shape, "o")
+    o_st = _dev_rows(o, torch.bfloat16, "o")
+    if lse is not None:
+        _shape(lse, (B, Hq, N), "lse")
+        _dev_tensor(lse, torch.float32, "lse")
+    a = CacheAttnArgs(cache.args, _ptr(seq), _ptr(q), _ptr(o), q_st, o_st, _ptr(lse), Hq, N,
+                      _ptr(counts), int(frame), int(window),
+                      1.0 / math.sqrt(d) if scale is None else float(scale), None, 0)
+    need = lib.salad_cache_attn_workspace_bytes(ctypes.byref(a))
+    if need:
+        ws = _empty_on(stream, lambda: _workspace(need, q.device, workspace))
+        a.workspace, a.workspace_bytes = _ptr(ws), ws.numel() * ws.element_size()
+    _check(lib.salad_cache_attn(ctypes.byref(a), _stream(stream)), "salad_cache_attn")
+    return o
 
 
 def permute_tokens(src: torch.Tensor, F: int, Hh: int, Wh: int, *, inverse: bool = False,

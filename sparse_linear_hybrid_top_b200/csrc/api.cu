@@ -894,6 +894,162 @@ salad_status salad_rope(const salad_rope_args* a, salad_stream stream) {
   return from_cuda(launch_rope(c, r));
 }
 
+// ----------------------------------------------------------- block cache --
+namespace {
+
+salad_status check_cache(const salad_cache& c) {
+  if (c.B < 1 || c.H < 1 || c.H > kMaxHeads || c.B > 65535 ||
+      static_cast<long long>(c.B) * c.H > 65535)
+    return SALAD_ERR_INVALID_ARG;
+  if (c.d != 64 && c.d != 128) return SALAD_ERR_UNSUPPORTED;
+  if (c.pages < 1 || c.blocks < 1 || c.blocks > (1 << 24)) return SALAD_ERR_INVALID_ARG;
+  if (!aligned(c.k_pages, 16) || !aligned(c.v_pages, 16) || !aligned(c.k_tail, 16) ||
+      !aligned(c.v_tail, 16) || !aligned(c.k_scale, 4) || !aligned(c.v_scale, 4) ||
+      !aligned(c.page_table, 4))
+    return SALAD_ERR_INVALID_ARG;
+  return SALAD_OK;
+}
+
+CacheView cache_view(const salad_cache& c) {
+  CacheView v;
+  v.k_pages = static_cast<unsigned char*>(c.k_pages);
+  v.v_pages = static_cast<unsigned char*>(c.v_pages);
+  v.k_scale = c.k_scale;
+  v.v_scale = c.v_scale;
+  v.k_tail = c.k_tail;
+  v.v_tail = c.v_tail;
+  v.page_table = c.page_table;
+  v.B = c.B; v.H = c.H; v.d = c.d;
+  v.pages = c.pages; v.blocks = c.blocks;
+  return v;
+}
+
+// Whether a tensor shares memory with one of the cache's buffers.
+bool in_cache(const salad_cache& c, const Strided& t) {
+  const size_t page = static_cast<size_t>(c.pages) * c.H * 64 * c.d;
+  const size_t tail = static_cast<size_t>(c.B) * 2 * c.H * 64 * c.d * 2;
+  const size_t scale = static_cast<size_t>(c.pages) * c.H * 4;
+  const size_t n = static_cast<size_t>(t.extent());
+  return overlaps(t.base, n, c.k_pages, page) || overlaps(t.base, n, c.v_pages, page) ||
+         overlaps(t.base, n, c.k_tail, tail) || overlaps(t.base, n, c.v_tail, tail) ||
+         overlaps(t.base, n, c.k_scale, scale) || overlaps(t.base, n, c.v_scale, scale);
+}
+
+}  // namespace
+
+salad_status salad_cache_append(const salad_cache_append_args* a, salad_stream stream) {
+  if (a == nullptr) return SALAD_ERR_INVALID_ARG;
+  const salad_cache& cc = a->cache;
+  salad_status st = check_cache(cc);
+  if (st != SALAD_OK) return st;
+  if (a->N < 1 || a->N > kMaxN) return SALAD_ERR_INVALID_ARG;
+  if (!aligned(a->seq, 4)) return SALAD_ERR_INVALID_ARG;
+  if (a->seq_out != nullptr &&
+      (!aligned(a->seq_out, 4) ||
+       (a->seq_out != a->seq &&
+        overlaps(a->seq_out, static_cast<size_t>(cc.B) * 8, a->seq, static_cast<size_t>(cc.B) * 8))))
+    return SALAD_ERR_INVALID_ARG;
+  if (a->counts != nullptr && !aligned(a->counts, 4)) return SALAD_ERR_INVALID_ARG;
+  if (a->rotate != 0 && a->rotate != 1) return SALAD_ERR_INVALID_ARG;
+  if (a->rotate &&
+      (st = check_rotation(a->positions, a->positions_batched, a->Hh, a->Wh, a->split, cc.d, a->base,
+                           a->pairing)) != SALAD_OK)
+    return st;
+  const Strided k = strided(a->k, a->k_st, cc.B, cc.H, a->N, cc.d * 2, 2);
+  const Strided v = strided(a->v, a->v_st, cc.B, cc.H, a->N, cc.d * 2, 2);
+  if (!strides_ok(k) || !strides_ok(v) || in_cache(cc, k) || in_cache(cc, v))
+    return SALAD_ERR_INVALID_ARG;
+  Ctx c;
+  if ((st = get_ctx(stream, &c)) != SALAD_OK) return st;
+  CacheAppendArgs p;
+  std::memset(&p, 0, sizeof(p));
+  p.cache = cache_view(cc);
+  p.seq = a->seq;
+  p.seq_out = a->seq_out;
+  p.k = a->k;
+  p.v = a->v;
+  for (int i = 0; i < 3; ++i) {
+    p.k_st[i] = k.stride[i] / 2;
+    p.v_st[i] = v.stride[i] / 2;
+    p.split[i] = a->split[i];
+  }
+  p.N = a->N;
+  p.counts = a->counts;
+  p.rotate = a->rotate;
+  p.where = RopeWhere{a->positions, a->positions_batched ? 3ll * a->N : 0ll, a->Hh, a->Wh, 0};
+  p.base = a->base;
+  p.pairing = a->rotate ? a->pairing : 0;
+  return from_cuda(launch_cache_append(c, p));
+}
+
+namespace {
+
+// Checks of everything but the workspace; fills p.
+salad_status check_cache_attn(const salad_cache_attn_args* a, CacheAttnArgs* p) {
+  if (a == nullptr) return SALAD_ERR_INVALID_ARG;
+  const salad_cache& cc = a->cache;
+  const salad_status st = check_cache(cc);
+  if (st != SALAD_OK) return st;
+  if (a->N < 1 || a->N > kMaxN || a->Hq < 1 || a->Hq > kMaxHeads || a->Hq % cc.H != 0)
+    return SALAD_ERR_INVALID_ARG;
+  if (!aligned(a->seq, 4) || (a->counts != nullptr && !aligned(a->counts, 4)) ||
+      (a->lse != nullptr && !aligned(a->lse, 4)))
+    return SALAD_ERR_INVALID_ARG;
+  if (a->frame < 0 || !(a->scale > 0.0f) || !std::isfinite(a->scale)) return SALAD_ERR_INVALID_ARG;
+  const Strided q = strided(a->q, a->q_st, cc.B, a->Hq, a->N, cc.d * 2, 2);
+  const Strided o = strided(a->o, a->o_st, cc.B, a->Hq, a->N, cc.d * 2, 2);
+  if (!strides_ok(q) || !strides_ok(o) || !distinct(o) || !disjoint(q, o) || in_cache(cc, o))
+    return SALAD_ERR_INVALID_ARG;
+  if (a->lse != nullptr) {
+    const size_t n = static_cast<size_t>(cc.B) * a->Hq * a->N * 4;
+    if (overlaps(a->lse, n, q.base, static_cast<size_t>(q.extent())) ||
+        overlaps(a->lse, n, o.base, static_cast<size_t>(o.extent())))
+      return SALAD_ERR_INVALID_ARG;
+  }
+  std::memset(p, 0, sizeof(*p));
+  p->cache = cache_view(cc);
+  p->seq = a->seq;
+  p->q = a->q;
+  p->o = a->o;
+  for (int i = 0; i < 3; ++i) {
+    p->q_st[i] = q.stride[i] / 2;
+    p->o_st[i] = o.stride[i] / 2;
+  }
+  p->lse = a->lse;
+  p->Hq = a->Hq;
+  p->N = a->N;
+  p->counts = a->counts;
+  p->frame = a->frame;
+  p->window = a->window;
+  p->scale = a->scale;
+  p->workspace = a->workspace;
+  return SALAD_OK;
+}
+
+}  // namespace
+
+size_t salad_cache_attn_workspace_bytes(const salad_cache_attn_args* a) {
+  CacheAttnArgs p;
+  if (check_cache_attn(a, &p) != SALAD_OK) return 0;
+  Ctx c;
+  c.num_sms = 148;   // a B200's, where no device is current
+  get_ctx(nullptr, &c);
+  return cache_attn_ws_bytes(p, c.num_sms);
+}
+
+salad_status salad_cache_attn(const salad_cache_attn_args* a, salad_stream stream) {
+  CacheAttnArgs p;
+  salad_status st = check_cache_attn(a, &p);
+  if (st != SALAD_OK) return st;
+  Ctx c;
+  c.num_sms = 148;
+  const salad_status device = get_ctx(stream, &c);
+  if ((st = check_ws(a->workspace, a->workspace_bytes, cache_attn_ws_bytes(p, c.num_sms))) != SALAD_OK)
+    return st;
+  if (device != SALAD_OK) return device;
+  return from_cuda(launch_cache_attn(c, p));
+}
+
 // ------------------------------------------------------------- errors --
 salad_status salad_check_error(salad_stream stream) {
   Ctx c;
@@ -907,7 +1063,8 @@ salad_status salad_check_error(salad_stream stream) {
     const unsigned zero = 0;
     if (cudaMemcpy(c.err, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess)
       return SALAD_ERR_CUDA;
-    return (word & kErrTimeout) ? SALAD_ERR_TIMEOUT : SALAD_ERR_CUDA;
+    if (word & kErrTimeout) return SALAD_ERR_TIMEOUT;
+    return (word & kErrLayout) ? SALAD_ERR_CUDA : SALAD_ERR_INVALID_ARG;
   }
   return SALAD_OK;
 }

@@ -17,6 +17,7 @@ namespace salad {
 // Device error bits, OR-ed into the library's error word.
 constexpr unsigned kErrTimeout = 1u;   // a bounded wait ran out
 constexpr unsigned kErrLayout = 2u;    // a kernel found its shared memory misaligned
+constexpr unsigned kErrRange = 4u;     // a cache operator skipped a page, length or count out of range
 
 // ------------------------------------------------------------------ misc --
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

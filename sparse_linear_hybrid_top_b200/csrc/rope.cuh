@@ -37,17 +37,41 @@ __device__ __forceinline__ int3 rope_position(const RopeWhere& w, int b, int n, 
   return make_int3(line / w.Hh, line % w.Hh, p - line * w.Wh);
 }
 
-// (cos, sin) of 2 pi * pos * turns.  The product and the reduction to
-// [-1/2, 1/2] turns are float64: |pos| < 2^31 and rates below 1/(2 pi) leave an
-// error under 2^-25 turns at the farthest position and under 2^-44 within
-// 4096.  The reduced turn is rounded to float32 once (2^-25 of a turn at
-// most), where sincospif is accurate to an ulp.
+// (cos, sin) of 2 pi * pos * turns, float64 rounded once to float32.
+// |pos| < 2^31 and rates of at most 1/(2 pi) keep the product below 2^29
+// turns, so adding and taking off 1.5 * 2^52 rounds it to whole turns and to
+// quarters exactly.  What is left, z in [-pi/4, pi/4], goes into the Taylor
+// polynomials of sine and cosine through z^13 and z^14, whose next terms are
+// below 2^-45.  22 float64 operations per token and pair, some 1% of a head's
+// time each: the bits do not depend on a fast sine's error, and a key lands on
+// the same 8-bit code as one that is turned in float64.
 __device__ __forceinline__ float2 rope_cos_sin(double turns, int pos) {
+  constexpr double kWhole = 6755399441055744.0;   // 1.5 * 2^52
   const double a = static_cast<double>(pos) * turns;
-  const float r = static_cast<float>(2.0 * (a - rint(a)));
-  float sn, cs;
-  sincospif(r, &sn, &cs);
-  return make_float2(cs, sn);
+  const double t = a - ((a + kWhole) - kWhole);
+  const double fourth = t * 4.0 + kWhole;
+  const int quadrant = __double2loint(fourth);
+  const double z = (t - (fourth - kWhole) * 0.25) * 6.283185307179586;
+  const double z2 = z * z;
+  double s = 1.0 / 6227020800.0;
+  s = fma(s, z2, -1.0 / 39916800.0);
+  s = fma(s, z2, 1.0 / 362880.0);
+  s = fma(s, z2, -1.0 / 5040.0);
+  s = fma(s, z2, 1.0 / 120.0);
+  s = fma(s, z2, -1.0 / 6.0);
+  s = fma(s * z2, z, z);
+  double c = -1.0 / 87178291200.0;
+  c = fma(c, z2, 1.0 / 479001600.0);
+  c = fma(c, z2, -1.0 / 3628800.0);
+  c = fma(c, z2, 1.0 / 40320.0);
+  c = fma(c, z2, -1.0 / 720.0);
+  c = fma(c, z2, 1.0 / 24.0);
+  c = fma(c, z2, -0.5);
+  c = fma(c, z2, 1.0);
+  const float fs = static_cast<float>(s), fc = static_cast<float>(c);
+  // Quarter turns: (cos, sin) -> (-sin, cos) each.
+  const float x = quadrant & 1 ? -fs : fc, y = quadrant & 1 ? fc : fs;
+  return quadrant & 2 ? make_float2(-x, -y) : make_float2(x, y);
 }
 
 // The rotated pair.  Products and sums are rounded one by one (no fused

@@ -2,13 +2,13 @@
 with a float64 implementation.
 
 Tolerances.  A result is rounded once to the tensors' type: half a step,
-eps(type) / 2 relative.  Before that the kernel works in float32 on a cosine
-and a sine whose reduced turn carries 2^-25 of a turn (2 pi 2^-25 rad =
-1.9e-7), an ulp of sincospi (1.2e-7) and, at far positions, what float64
-leaves of |pos| / (2 pi) turns (|pos| 2^-53, twice: the rate and the product);
-products and sum add 3 * 2^-24.  So, for a pair (u, w) with |x| = max(|u|, |w|),
-    |err| <= eps/2 |y| + |x| (2 (1.9e-7 + 1.2e-7 + 2 pi * 2 |pos| 2^-53 / (2 pi)) + 3 * 6e-8 * 2).
-The bound below takes 1.1e-6 |x| + 4 |pos| 2^-53 |x| for the second part.
+eps(type) / 2 relative.  Before that the kernel multiplies float32 values by a
+cosine and a sine rounded once to float32 (2^-24 relative) from an angle of
+which float64 leaves 2 * 2^-53 |pos| rad at far positions (the rate's and the
+product's rounding); two products and a sum add 3 * 2^-24.  So, for a pair
+(u, w) with |x| = max(|u|, |w|), the second part is at most
+    |x| (2 * 2^-24 + 2 * 2 |pos| 2^-53 + 2 * 3 * 2^-24) < |x| (4.8e-7 + 4 |pos| 2^-53),
+taken as 1.1e-6 |x| + 4 |pos| 2^-53 |x|.
 """
 import ctypes
 import math
