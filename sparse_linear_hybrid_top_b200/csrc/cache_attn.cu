@@ -484,7 +484,13 @@ cudaError_t launch_d(const Ctx& c, const CacheAttnParams& P, const Shape& s) {
 
 }  // namespace
 
+// Rows of a (sequence, key head) from which the tensor-core kernel takes over.
+static bool many_rows(const CacheAttnArgs& a) {
+  return static_cast<long long>(a.Hq / a.cache.H) * a.N > 64;
+}
+
 size_t cache_attn_ws_bytes(const CacheAttnArgs& a, int num_sms) {
+  if (many_rows(a)) return cache_attn_tc_ws_bytes(a, num_sms);
   const Shape s = shape_of(a, num_sms);
   if (s.splits == 1) return 0;
   const size_t rows = static_cast<size_t>(s.rows) * s.splits;
@@ -492,7 +498,6 @@ size_t cache_attn_ws_bytes(const CacheAttnArgs& a, int num_sms) {
 }
 
 cudaError_t launch_cache_attn(const Ctx& c, const CacheAttnArgs& a) {
-  const Shape s = shape_of(a, c.num_sms);
   CacheAttnParams P;
   P.c = a.cache;
   P.seq = a.seq;
@@ -508,17 +513,19 @@ cudaError_t launch_cache_attn(const Ctx& c, const CacheAttnArgs& a) {
   P.frame = a.frame;
   P.window = a.window;
   P.scale_log2 = a.scale * 1.4426950408889634f;
-  P.tiles = s.tiles;
-  P.splits = s.splits;
+  P.err = c.err;
+  P.wait_ns = c.wait_ns;
   P.part_o = nullptr;
   P.part_ml = nullptr;
+  if (many_rows(a)) return launch_cache_attn_tc(c, a, P);
+  const Shape s = shape_of(a, c.num_sms);
+  P.tiles = s.tiles;
+  P.splits = s.splits;
   if (s.splits > 1) {
     const size_t rows = static_cast<size_t>(s.rows) * s.splits;
     P.part_o = static_cast<float*>(a.workspace);
     P.part_ml = reinterpret_cast<float2*>(static_cast<char*>(a.workspace) + align256(rows * a.cache.d * sizeof(float)));
   }
-  P.err = c.err;
-  P.wait_ns = c.wait_ns;
   return a.cache.d == 128 ? launch_d<128>(c, P, s) : launch_d<64>(c, P, s);
 }
 

@@ -74,4 +74,7 @@ __device__ __forceinline__ CacheRow cache_row(const CacheAttnParams& P, int r, i
   return x;
 }
 
+size_t cache_attn_tc_ws_bytes(const CacheAttnArgs& a, int num_sms);
+cudaError_t launch_cache_attn_tc(const Ctx& c, const CacheAttnArgs& a, CacheAttnParams P);
+
 }  // namespace salad
