@@ -7,12 +7,14 @@
 // tile of codes is read and turned into bf16 once per 256 rows.  A key tile is
 // 128 keys (two blocks).
 //
-// Warp roles (416 threads, one CTA per SM):
+// Warp roles (512 threads, one CTA per SM; warps 13..15 only fill the last
+// warpgroup, whose registers the others take):
 //   warps 0..3, 4..7   softmax and output of slots 0 and 1, a row per thread
 //                      (warp w on TMEM lane quarter w % 4); they also load
 //                      their slot's rows of Q
 //   warps 8..11        codes -> bf16: global loads one operand tile ahead,
-//                      conversion in registers, 128-byte-swizzled stores
+//                      conversion in registers, 128-byte-swizzled stores; they
+//                      also pass the blocks' scales to the softmax warps
 //   warp 12            TMEM allocation and the single MMA-issuing thread
 // While the tensor pipe runs one slot's PV(t) and QK(t+1), the other slot's
 // softmax runs.  P overwrites S in TMEM as bf16.
@@ -33,7 +35,7 @@ namespace {
 
 constexpr int kRows = 256;            // query rows of an item
 constexpr int kTile = 128;            // keys of a tile
-constexpr int kThreads = 416;
+constexpr int kThreads = 512;       // four warpgroups, see the register shares
 
 template <int D>
 struct CT {
@@ -42,7 +44,8 @@ struct CT {
   static constexpr int kOperand = kSlabs * kRowSlab;    // 128 rows of Q, K or V
   static constexpr int kStages = 4;
   static constexpr int kBarBytes = 256;
-  static constexpr int kUsed = 2 * kOperand + kStages * kOperand + kBarBytes;
+  static constexpr int kScaleBytes = 4 * 16 + 4 * 8;    // scales of four tiles (K, K, V, V), four parts' (tiles, slots)
+  static constexpr int kUsed = 2 * kOperand + kStages * kOperand + kBarBytes + kScaleBytes;
   // More than half of the SM's shared memory: one CTA (and its 512 TMEM columns) per SM.
   static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
@@ -219,6 +222,32 @@ __device__ __forceinline__ float max64(const float* v) {
   return fmax3(fmax3(b[0], b[1], b[2]), fmax3(b[3], b[4], b[5]), fmaxf(b[6], b[7]));
 }
 
+// Pairs of floats in one register pair (two operations an instruction).
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// What a block's products are scaled by: positive, so that -inf stays -inf
+// (under a NaN scale the scores that count are NaN already).
+__device__ __forceinline__ float key_factor(float scale_log2, float ks) {
+  return isnan(ks) ? 1.0f : fmaxf(scale_log2 * ks, 1e-37f);
+}
+
 // Channels in the order that e4m3_pairs leaves them: (0, 2, 1, 3) of each four.
 __device__ __forceinline__ uint4 reorder(uint4 v) {
   return make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632),
@@ -265,6 +294,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
   // odd_seg[i % 4] = i + 1: part i's open block holds a value that is not finite.
   volatile int* odd_seg = abort_flag + 1;
   static_assert((2 * NS + 11) * 8 + 4 + 4 + 16 <= C::kBarBytes, "barrier region");
+  // Scales of tile i's two blocks in entry i % 4: of the keys (0: no page, its
+  // keys do not count), then of the values.  A converting thread writes them
+  // before it hands over the tile's keys.  It reaches tile i + 4 only when the
+  // values of tile i + 3 are stored, over those of tile i + 1: both slots have
+  // read tile i's scales by then.
+  float4* scales = reinterpret_cast<float4*>(reinterpret_cast<unsigned char*>(bars) + C::kBarBytes);
+  // Tiles and slots of part i in entry i % 4, for the issuer: written and read
+  // like the scales (a part has a tile at least).
+  int2* part_info = reinterpret_cast<int2*>(scales + 4);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const unsigned long long wait_ns = P.wait_ns;
@@ -294,8 +332,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
 
-  if (warp == 12) {
-    if (lane == 0) {
+  // Register shares, 4 x 128 in all: 160 for each softmax warpgroup, 128 for
+  // the converting one, 64 for the issuer's.
+  if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == 12 && lane == 0) {
       // ===================================================== MMA issuer
       constexpr uint32_t idesc_qk = idesc_bf16(128, 128, false, false);
       constexpr uint32_t idesc_pv = idesc_bf16(128, D, false, true);
@@ -315,11 +356,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
         }
         mma_commit(s_full(slot));
       };
-      for (Seg g = seg_at(T, w0, w1 - w0); g.left > 0 && ok; g = seg_next(P, g)) {
-        const int slots = g.two ? 2 : 1, n = g.t1 - g.t0;
+      int left = static_cast<int>(w1 - w0);
+      for (int part_no = 0; left > 0 && ok; ++part_no) {
         // Stages of the part: K0 V0 K1 V1 ...
+        if (!wait_stage(at)) { ok = false; break; }
+        const int2 info = part_info[part_no % 4];
+        const int n = info.x, slots = info.y;
         for (int slot = 0; slot < slots && ok; ++slot) {
-          ok = mbar_wait(q_full(slot), qn[slot]++ & 1u, wait_ns, abort_flag) && (slot > 0 || wait_stage(at));
+          ok = mbar_wait(q_full(slot), qn[slot]++ & 1u, wait_ns, abort_flag);
           if (!ok) break;
           tc_fence_after();
           issue_qk(slot, at);
@@ -351,6 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
           }
         }
         at += 2 * n;
+        left -= n;
       }
       if (!ok) raise_timeout(P.err, abort_flag);
       mma_commit(drain);
@@ -364,8 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
     uint32_t at = 0;                            // operand tiles written so far
     int part_no = 0;
     bool ok = true;
-    uint4 raw[4][C::kSlabs];
-    // Codes of block x of a tile (row i / 2 == x), where it is a closed block.
+    // Codes of one operand tile: rows i of block i / 2.
     auto load = [&](uint4 (&to)[4][C::kSlabs], const unsigned char* pages, const int (&page)[2], int h) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -377,97 +421,143 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
           to[i][s] = pg == -2 ? make_uint4(0u, 0u, 0u, 0u) : __ldg(reinterpret_cast<const uint4*>(p + 64 * s));
       }
     };
-    // Pages of tile j's two blocks: -2 where the block is not closed.  A table
-    // entry that is no page reads page 0; the softmax masks its keys.
-    auto pages_of = [&](const Seg& g, int j, int (&page)[2]) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int blk = 2 * j + x;
-        page[x] = -2;
-        if (blk < g.s.len / kCacheBlock) {
-          page[x] = cache_page(__ldg(P.c.page_table + static_cast<long long>(g.b) * P.c.blocks + blk), P.c.pages);
-          if (page[x] < 0) {
-            if (lane == 0) atomicOr(P.err, kErrRange);
-            page[x] = 0;
-          }
+    // Pages and scales of 32 blocks, one per lane: -2 where the block is not
+    // closed.  A table entry that is no page reads page 0 with a key scale of
+    // 0, by which the softmax masks its keys.
+    struct Blocks {
+      int page;
+      float ks, vs;
+    };
+    auto blocks_at = [&](const Seg& g, int blk) {
+      Blocks k{-2, 1.0f, 1.0f};
+      if (blk + lane < g.s.len / kCacheBlock) {
+        k.page = cache_page(__ldg(P.c.page_table + static_cast<long long>(g.b) * P.c.blocks + blk + lane), P.c.pages);
+        if (k.page < 0) {
+          k.page = 0;
+          k.ks = 0.0f;
+        } else {
+          const long long at = static_cast<long long>(k.page) * P.c.H + g.h;
+          k.ks = __ldg(P.c.k_scale + at);
+          k.vs = __ldg(P.c.v_scale + at);
         }
       }
+      return k;
     };
-    auto store = [&](const uint4 (&from)[4][C::kSlabs], const Seg& g, int j, const int (&page)[2], bool value) -> bool {
+    auto pages_of = [&](const Blocks& k, int i, int (&page)[2]) {
+      page[0] = __shfl_sync(0xffffffffu, k.page, 2 * i);
+      page[1] = __shfl_sync(0xffffffffu, k.page, 2 * i + 1);
+    };
+    // The open block's rows over this thread's zeros of a tile, in bf16.  Values that are
+    // not finite would spread as 0 * inf; they are left to the rows that see
+    // them.  (Rolled up: the loop over closed tiles must stay in the
+    // instruction cache.)
+    auto store_open = [&](unsigned char* dst, const Seg& g, int half, bool value) {
+      const int held = g.s.len % kCacheBlock;
+      const __nv_bfloat16* tail = static_cast<const __nv_bfloat16*>(value ? P.c.v_tail : P.c.k_tail) +
+                                  ((static_cast<long long>(g.b) * 2 + g.s.slot) * P.c.H + g.h) * kCacheBlock * D;
+      bool odd = false;
+      // This thread's own rows and chunks of the half.
+#pragma unroll 1
+      for (int e = 0; e < 4 * C::kSlabs; ++e) {
+        const int row = r8 + 32 * (e & 1), c = 8 * (e >> 2) + 2 * c16 + ((e >> 1) & 1);
+        if (row >= held) continue;
+        uint4 x = reorder(__ldg(reinterpret_cast<const uint4*>(tail + row * D) + c));
+        if (value) {
+          const uint4 y = make_uint4(finite_or_zero(x.x), finite_or_zero(x.y), finite_or_zero(x.z), finite_or_zero(x.w));
+          odd = odd || y.x != x.x || y.y != x.y || y.z != x.z || y.w != x.w;
+          x = y;
+        }
+        const int at_row = 64 * half + row;
+        *reinterpret_cast<uint4*>(dst + (c / 8) * C::kRowSlab + at_row * 128 + (((c % 8) ^ (at_row & 7)) << 4)) = x;
+      }
+      if (odd) odd_seg[part_no % 4] = part_no + 1;
+    };
+    Seg g = seg_at(T, w0, w1 - w0);
+    uint32_t tile_no = 0;
+    // 16 tiles' blocks, and the 16 after them (loaded 16 tiles early).
+    Blocks cur = blocks_at(g, 2 * (g.all.first + g.t0)), nxt = cur;
+    int page[2];
+    pages_of(cur, 0, page);
+    uint4 raw[4][C::kSlabs];
+    load(raw, P.c.k_pages, page, g.h);
+    // One operand tile a turn, K and V of a tile after one another; the next
+    // one's loads are in flight while this one is converted.
+    int t = g.t0;
+    bool value = false, more = true;
+#pragma unroll 1
+    while (more && ok) {
+      const int j = g.all.first + t, i = (t - g.t0) % 16;
+      const int open = g.s.len / kCacheBlock - 2 * j;    // 0 or 1: the open block is that half
+      Seg ng = g;
+      int nt = t;
+      uint4 ahead[4][C::kSlabs];
+      if (!value) {
+        if (i == 0) nxt = blocks_at(g, 2 * j + 32);
+        const float k0 = __shfl_sync(0xffffffffu, cur.ks, 2 * i), k1 = __shfl_sync(0xffffffffu, cur.ks, 2 * i + 1);
+        const float v0 = __shfl_sync(0xffffffffu, cur.vs, 2 * i), v1 = __shfl_sync(0xffffffffu, cur.vs, 2 * i + 1);
+        if (w == 0 && lane == 0) {
+          if (t == g.t0) part_info[part_no % 4] = make_int2(g.t1 - g.t0, g.two ? 2 : 1);
+          scales[tile_no % 4] = make_float4(k0, k1, v0, v1);
+          if (k0 == 0.0f || k1 == 0.0f) atomicOr(P.err, kErrRange);
+        }
+      } else {
+        ++nt;
+        if (nt == g.t1) {
+          ng = seg_next(P, g);
+          more = ng.left > 0;
+          nt = ng.t0;
+          if (more) cur = blocks_at(ng, 2 * (ng.all.first + nt));
+          pages_of(cur, 0, page);
+        } else {
+          if (i == 15) cur = nxt;
+          pages_of(cur, (i + 1) % 16, page);
+        }
+      }
+      if (more) load(ahead, value ? P.c.k_pages : P.c.v_pages, page, ng.h);
+      // Store this one, once the MMAs that read its stage have run.
       const int st = static_cast<int>(at % NS);
       const uint32_t n = at / NS;
-      if (n > 0 && !__all_sync(0xffffffffu, mbar_wait(empty(st), (n - 1) & 1u, wait_ns, abort_flag))) return false;
+      if (n > 0 && !__all_sync(0xffffffffu, mbar_wait(empty(st), (n - 1) & 1u, wait_ns, abort_flag))) {
+        ok = false;
+        break;
+      }
       unsigned char* dst = ring + st * C::kOperand;
-      bool odd = false;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = r8 + 32 * i;
-        const bool open = page[i / 2] == -2 && 2 * j + i / 2 == g.s.len / kCacheBlock;
+      for (int x = 0; x < 4; ++x) {
+        const int row = r8 + 32 * x;
 #pragma unroll
         for (int s = 0; s < C::kSlabs; ++s) {
           uint4 lo, hi;
-          e4m3_pairs(from[i][s].x, lo.x, lo.y);
-          e4m3_pairs(from[i][s].y, lo.z, lo.w);
-          e4m3_pairs(from[i][s].z, hi.x, hi.y);
-          e4m3_pairs(from[i][s].w, hi.z, hi.w);
-          if (open && row % 64 < g.s.len % kCacheBlock) {
-            // The open block's rows, in bf16.  Values that are not finite
-            // would spread as 0 * inf; they are left to the rows that see them.
-            const uint4* t = reinterpret_cast<const uint4*>(
-                static_cast<const __nv_bfloat16*>(value ? P.c.v_tail : P.c.k_tail) +
-                (((static_cast<long long>(g.b) * 2 + g.s.slot) * P.c.H + g.h) * kCacheBlock + row % 64) * D + 64 * s + 16 * c16);
-            lo = reorder(t[0]);
-            hi = reorder(t[1]);
-            if (value) {
-              uint32_t* x[8] = {&lo.x, &lo.y, &lo.z, &lo.w, &hi.x, &hi.y, &hi.z, &hi.w};
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const uint32_t f = finite_or_zero(*x[e]);
-                odd = odd || f != *x[e];
-                *x[e] = f;
-              }
-            }
-          }
+          e4m3_pairs(raw[x][s].x, lo.x, lo.y);
+          e4m3_pairs(raw[x][s].y, lo.z, lo.w);
+          e4m3_pairs(raw[x][s].z, hi.x, hi.y);
+          e4m3_pairs(raw[x][s].w, hi.z, hi.w);
           unsigned char* to = dst + s * C::kRowSlab + row * 128;
           *reinterpret_cast<uint4*>(to + (((2 * c16) ^ (row & 7)) << 4)) = lo;
           *reinterpret_cast<uint4*>(to + (((2 * c16 + 1) ^ (row & 7)) << 4)) = hi;
         }
       }
-      if (odd) odd_seg[part_no % 4] = part_no + 1;
+      if (open == 0 || open == 1) store_open(dst, g, open, value);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(full(st));
       ++at;
-      return true;
-    };
-    Seg g = seg_at(T, w0, w1 - w0);
-    int page[2], next_page[2];
-    pages_of(g, g.all.first + g.t0, page);
-    load(raw, P.c.k_pages, page, g.h);
-    while (g.left > 0 && ok) {
-      Seg ng = g;
-      for (int t = g.t0; t < g.t1 && ok; ++t) {
-        const int j = g.all.first + t;
-        const bool last = t + 1 == g.t1;
-        if (last) ng = seg_next(P, g);
-        const bool more = !last || ng.left > 0;
-        const Seg& f = last ? ng : g;            // where the next tile is
-        if (more) pages_of(f, last ? ng.all.first + ng.t0 : j + 1, next_page);
-        uint4 ahead[4][C::kSlabs];
-        load(ahead, P.c.v_pages, page, g.h);
-        ok = store(raw, g, j, page, false);
-        if (!ok) break;
-        if (more) load(raw, P.c.k_pages, next_page, f.h);
-        ok = store(ahead, g, j, page, true);
-        page[0] = next_page[0];
-        page[1] = next_page[1];
+      if (value) {
+        ++tile_no;
+        if (t + 1 == g.t1) ++part_no;
+        g = ng;
+        t = nt;
       }
-      ++part_no;
-      g = ng;
+      value = !value;
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int s = 0; s < C::kSlabs; ++s) raw[x][s] = ahead[x][s];
     }
     if (!ok) raise_timeout(P.err, abort_flag);
   } else {
     // ============================================ softmax and output
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
     const int slot = warp / 4, quarter = warp % 4;
     const int r = quarter * 32 + lane;                  // row of the slot (TMEM lane)
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -488,20 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full(slot));
     };
-    // Scales of tile j's two blocks: of the keys (0 where its keys do not
-    // count: no page) and of the values; 1 for the open block.
-    auto scales_of = [&](const Seg& g, int j, float (&ks)[2], float (&vs)[2]) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int blk = 2 * j + x;
-        ks[x] = vs[x] = 1.0f;
-        if (blk < g.s.len / kCacheBlock) {
-          const int pg = cache_page(__ldg(P.c.page_table + static_cast<long long>(g.b) * P.c.blocks + blk), P.c.pages);
-          ks[x] = pg < 0 ? 0.0f : __ldg(P.c.k_scale + static_cast<long long>(pg) * P.c.H + g.h);
-          vs[x] = pg < 0 ? 1.0f : __ldg(P.c.v_scale + static_cast<long long>(pg) * P.c.H + g.h);
-        }
-      }
-    };
+    uint32_t tile_no = 0;                               // of the CTA
     Seg g = seg_at(T, w0, w1 - w0);
     int part_no = 0;
     // A slot without rows takes no part in an item; the next item of the CTA
@@ -515,61 +592,59 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
         const int n = g.t1 - g.t0;
         float m = -INFINITY, l = 0.0f;
         bool vbad = false;
-        float ks[2], vs[2], nks[2], nvs[2];
-        scales_of(g, g.all.first + g.t0, ks, vs);
         for (int t = 0; t < n; ++t) {
           const int j = g.all.first + g.t0 + t;
-          if (t + 1 < n) scales_of(g, j + 1, nks, nvs);   // travels while this tile is processed
           if (!__all_sync(0xffffffffu, mbar_wait(s_full(slot), sn & 1u, wait_ns, abort_flag))) {
             ok = false;
             break;
           }
           ++sn;
           tc_fence_after();
-          float c2[2], ev[2];
-          int lo[2], hi[2];
-          bool any[2], partial[2], k_nan[2];
-#pragma unroll
+          const float4 sc = scales[(tile_no + t) % 4];
+          // Halves outside some row's range: scores there become -inf, in
+          // TMEM.  (A NaN key scale makes the scores that are seen NaN.)  The
+          // halves' loops are rolled up: the code of a whole tile, beside
+          // the converting warps', must stay in the instruction cache.
+          uint32_t any = 0;
+#pragma unroll 1
           for (int x = 0; x < 2; ++x) {
             const int kb = j * kTile + 64 * x;
-            lo[x] = row.see.lo - kb;
-            hi[x] = ks[x] == 0.0f ? -1 : row.see.end - 1 - kb;
-            const bool live = lo[x] < 64 && hi[x] >= 0 && row.see.end > 0;
-            if (!live) hi[x] = -1;
-            k_nan[x] = isnan(ks[x]);
-            c2[x] = k_nan[x] ? 1.0f : fmaxf(P.scale_log2 * ks[x], 1e-37f);   // positive: -inf stays -inf
-            if (isnan(vs[x])) {
-              vbad = vbad || live;
-              vs[x] = 1.0f;
-            }
-            ev[x] = pow2_log(vs[x]);
-            any[x] = __any_sync(0xffffffffu, live);
-            partial[x] = k_nan[x] || __any_sync(0xffffffffu, !(lo[x] <= 0 && hi[x] >= 63));
-          }
-          // Scores of one half outside the row's range count as -inf.
-          auto masked = [&](float (&sv)[64], int x) {
+            const float ks = x ? sc.y : sc.x, vs = x ? sc.w : sc.z;
+            const int lo = row.see.lo - kb, hi = ks == 0.0f ? -1 : row.see.end - 1 - kb;
+            const bool live = lo < 64 && hi >= 0 && row.see.end > 0;
+            vbad = vbad || (live && isnan(vs));
+            if (!__any_sync(0xffffffffu, live)) continue;
+            any |= 1u << x;
+            if (!isnan(ks) && __all_sync(0xffffffffu, live && lo <= 0 && hi >= 63)) continue;
+            const float seen = isnan(ks) ? ks : 0.0f;
+#pragma unroll 1
+            for (int c0 = 0; c0 < 64; c0 += 32) {
+              uint32_t s32[32];
+              tmem_ld32(sbuf + 64 * x + c0, s32);
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
-              sv[c] = c >= lo[x] && c <= hi[x] ? (k_nan[x] ? __int_as_float(0x7fffffff) : sv[c]) : -INFINITY;
-          };
+              for (int c = 0; c < 32; ++c)
+                s32[c] = live && c0 + c >= lo && c0 + c <= hi ? __float_as_uint(__uint_as_float(s32[c]) + seen) : 0xff800000u;
+              tmem_st32(sbuf + 64 * x + c0, s32);
+            }
+            tmem_st_wait();
+          }
           // Pass 1: the row's maximum.
           float pm = -INFINITY;
-#pragma unroll
+#pragma unroll 1
           for (int x = 0; x < 2; ++x) {
-            if (!any[x]) continue;
+            if (!(any >> x & 1u)) continue;
             uint32_t s64[64];
             tmem_ld64(sbuf + 64 * x, s64);
             float sv[64];
 #pragma unroll
             for (int c = 0; c < 64; ++c) sv[c] = __uint_as_float(s64[c]);
-            if (partial[x]) masked(sv, x);
-            pm = fmaxf(pm, max64(sv) * c2[x]);
+            pm = fmaxf(pm, max64(sv) * key_factor(P.scale_log2, x ? sc.y : sc.x));
           }
           // The maximum is raised lazily: O is rescaled only when it grows by
           // more than 2^8 (by anything under scales so large that P times 2^8
           // would leave float32).
           float f = 1.0f;
-          const float slack = fmaxf(ev[0], ev[1]) > 100.0f ? 0.0f : 8.0f;
+          const float slack = fmaxf(sc.z, sc.w) > 0x1p100f ? 0.0f : 8.0f;
           if (pm > m + slack) {
             f = m == -INFINITY ? 1.0f : ex2_ftz(m - pm);
             l *= f;
@@ -577,30 +652,34 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
           }
           const float nm = m == -INFINITY ? 0.0f : -m;
           // Pass 2: P = 2^(s c2 - m + ev) over the first 64 columns of S.
-#pragma unroll
+#pragma unroll 1
           for (int x = 0; x < 2; ++x) {
             uint32_t pk[32];
-            if (any[x]) {
+            if (any >> x & 1u) {
+              const float vs0 = x ? sc.w : sc.z;
+              const float vs = isnan(vs0) ? 1.0f : vs0;
+              const float c2 = key_factor(P.scale_log2, x ? sc.y : sc.x);
+              const uint64_t c22 = pack2(c2, c2), off = pack2(nm + pow2_log(vs), nm + pow2_log(vs));
               uint32_t s64[64];
               tmem_ld64(sbuf + 64 * x, s64);
-              float sv[64];
-#pragma unroll
-              for (int c = 0; c < 64; ++c) sv[c] = __uint_as_float(s64[c]);
-              if (partial[x]) masked(sv, x);
-              const float off = nm + ev[x];
-              float a0 = 0.0f, a1 = 0.0f, a2 = 0.0f, a3 = 0.0f;
+              uint64_t a0 = 0, a1 = 0;
 #pragma unroll
               for (int c = 0; c < 64; c += 4) {
-                const float p0 = ex2_ftz(fmaf(sv[c], c2[x], off)), p1 = ex2_ftz(fmaf(sv[c + 1], c2[x], off));
-                const float p2 = ex2_ftz(fmaf(sv[c + 2], c2[x], off)), p3 = ex2_ftz(fmaf(sv[c + 3], c2[x], off));
+                float p0, p1, p2, p3;
+                unpack2(fma2(pack2(__uint_as_float(s64[c]), __uint_as_float(s64[c + 1])), c22, off), p0, p1);
+                unpack2(fma2(pack2(__uint_as_float(s64[c + 2]), __uint_as_float(s64[c + 3])), c22, off), p2, p3);
+                p0 = ex2_ftz(p0);
+                p1 = ex2_ftz(p1);
+                p2 = ex2_ftz(p2);
+                p3 = ex2_ftz(p3);
                 pk[c / 2] = pack_bf16x2(p0, p1);
                 pk[c / 2 + 1] = pack_bf16x2(p2, p3);
-                a0 += p0;
-                a1 += p1;
-                a2 += p2;
-                a3 += p3;
+                a0 = add2(a0, pack2(p0, p1));
+                a1 = add2(a1, pack2(p2, p3));
               }
-              l = fmaf((a0 + a1) + (a2 + a3), pow2_inv(vs[x]), l);
+              float s0, s1;
+              unpack2(add2(a0, a1), s0, s1);
+              l = fmaf(s0 + s1, pow2_inv(vs), l);
             } else {
 #pragma unroll
               for (int e = 0; e < 32; ++e) pk[e] = 0u;
@@ -618,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
             tc_fence_after();
           }
           if (t > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
-#pragma unroll
+#pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
               uint32_t o32[32];
               tmem_ld32(obuf + c0, o32);
@@ -631,8 +710,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(p_full(slot));
-          ks[0] = nks[0]; ks[1] = nks[1];
-          vs[0] = nvs[0]; vs[1] = nvs[1];
         }
         if (!ok) break;
         // Every QK of the part has run: the next part's Q, while its last PV does.
@@ -654,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
         const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
         char* orow = P.o + g.b * P.ob + row.head * P.oh + row.n * P.on;
         const long long part_row = (2ll * blockIdx.x + (g.first ? 0 : 1)) * kRows + slot * 128 + r;
-#pragma unroll
+#pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
           uint32_t o32[32];
           tmem_ld32(obuf + c0, o32);
@@ -696,6 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
         // No rows in this item: its slot's Q buffer is idle.
         load_q(ng);
       }
+      tile_no += g.t1 - g.t0;
       ++part_no;
       g = ng;
     }
