@@ -2,32 +2,42 @@
 // over the 8-bit block cache, on tcgen05 tensor cores.
 //
 // Bound by the tensor pipe (4 d operations per query row, key and head) and,
-// close behind it, by the exponentials.  A work item is 256 query rows of one
-// sequence and key head: two 128-row slots that share every key tile, so each
-// tile of codes is read and turned into bf16 once per 256 rows.  A key tile is
-// 128 keys (two blocks).
+// as tightly, by the exponentials: a 128 x 128 tile of scores takes its two
+// products 1024 cycles and its 16384 exponentials 1024 (16 lanes a cycle).  A
+// work item is 256 query rows of one sequence and key head: two 128-row slots
+// that share every key tile, so each tile of codes is converted once per 256
+// rows.  A key tile is 128 keys (two blocks).
 //
-// Warp roles (512 threads, one CTA per SM; warps 13..15 only fill the last
-// warpgroup, whose registers the others take):
+// Operands are fp16, in which every e4m3 code is exact and converts in one
+// instruction per pair (the bf16 route takes nine per four codes; the ALU
+// pipe runs both at 16 lanes a cycle).  A query row is scaled by a power of
+// two to a largest magnitude in [2^14, 2^15): its bf16 values stay exact down
+// to 2^-28 of that, and those below err by 2^-39 of it.  The open block's bf16
+// rows are scaled like a closed block's.  Key scales and the row's join the
+// softmax scale.  P, times the value block's scale, is at most 2^8 in fp16
+// (rounded by 2^-11); see the softmax for how its maximum and the row sum are
+// kept apart.
+//
+// Warp roles (384 threads, one CTA per SM):
 //   warps 0..3, 4..7   softmax and output of slots 0 and 1, a row per thread
 //                      (warp w on TMEM lane quarter w % 4); they also load
 //                      their slot's rows of Q
-//   warps 8..11        codes -> bf16: global loads one operand tile ahead,
-//                      conversion in registers, 128-byte-swizzled stores; they
-//                      also pass the blocks' scales to the softmax warps
-//   warp 12            TMEM allocation and the single MMA-issuing thread
+//   warp 8             TMEM allocation and the single MMA-issuing thread
+//   warps 9..11        codes -> fp16: from a ring of bulk-copied code tiles
+//                      to swizzled operand tiles; warp 9 also issues the bulk
+//                      copies, four operand tiles ahead, and passes the
+//                      blocks' scales to the softmax warps
 // While the tensor pipe runs one slot's PV(t) and QK(t+1), the other slot's
-// softmax runs.  P overwrites S in TMEM as bf16.
-//
-// The conversion leaves channels in the order (0, 2, 1, 3) within each group
-// of four.  Q is stored in that order too (the dot products do not change),
-// and the output's columns are put back when O is written.
+// softmax runs.  P overwrites S in TMEM.
 //
 // Balance: lengths are known on the device only, and tiles per item differ by
 // frame.  A first launch sums the items' tiles; every CTA then takes an equal
 // run of tiles, which may begin and end inside an item.  An item that one CTA
 // holds whole is written at once; the others leave float32 parts (two per
 // CTA at most), merged by a last launch.
+#include <cstring>
+#include <cuda_fp16.h>
+
 #include "cache_attn.cuh"
 
 namespace salad {
@@ -35,17 +45,20 @@ namespace {
 
 constexpr int kRows = 256;            // query rows of an item
 constexpr int kTile = 128;            // keys of a tile
-constexpr int kThreads = 512;       // four warpgroups, see the register shares
+constexpr int kThreads = 384;
 
 template <int D>
 struct CT {
   static constexpr int kSlabs = D / 64;
   static constexpr int kRowSlab = 128 * 128;            // 128 rows of 128 bytes
   static constexpr int kOperand = kSlabs * kRowSlab;    // 128 rows of Q, K or V
-  static constexpr int kStages = 4;
+  static constexpr int kStages = 3;                     // operand tiles
+  static constexpr int kRaw = 128 * D;                  // codes of an operand tile
+  static constexpr int kRaws = 4;
   static constexpr int kBarBytes = 256;
   static constexpr int kScaleBytes = 4 * 16 + 4 * 8;    // scales of four tiles (K, K, V, V), four parts' (tiles, slots)
-  static constexpr int kUsed = 2 * kOperand + kStages * kOperand + kBarBytes + kScaleBytes;
+  static constexpr int kSegBytes = 8 * 64;              // the softmax warps' current parts
+  static constexpr int kUsed = (2 + kStages) * kOperand + kRaws * kRaw + kBarBytes + kScaleBytes + kSegBytes;
   // More than half of the SM's shared memory: one CTA (and its 512 TMEM columns) per SM.
   static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
@@ -210,11 +223,13 @@ __device__ __forceinline__ Seg seg_next(const CacheAttnParams& P, const Seg& g) 
   return n;
 }
 
-__device__ __forceinline__ float max64(const float* v) {
+// Maximum of 64 values by a tree of three-input maxima (64 -> 22 -> 8 -> 3 -> 1).
+__device__ __forceinline__ float max64(const uint32_t* u) {
+  auto v = [&](int i) { return __uint_as_float(u[i]); };
   float a[22];
 #pragma unroll
-  for (int i = 0; i < 21; ++i) a[i] = fmax3(v[3 * i], v[3 * i + 1], v[3 * i + 2]);
-  a[21] = v[63];
+  for (int i = 0; i < 21; ++i) a[i] = fmax3(v(3 * i), v(3 * i + 1), v(3 * i + 2));
+  a[21] = v(63);
   float b[8];
 #pragma unroll
   for (int i = 0; i < 7; ++i) b[i] = fmax3(a[3 * i], a[3 * i + 1], a[3 * i + 2]);
@@ -242,16 +257,68 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// What a block's products are scaled by: positive, so that -inf stays -inf
-// (under a NaN scale the scores that count are NaN already).
-__device__ __forceinline__ float key_factor(float scale_log2, float ks) {
-  return isnan(ks) ? 1.0f : fmaxf(scale_log2 * ks, 1e-37f);
+// Two e4m3 codes as fp16 (exact).
+__device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t codes) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<unsigned short>(codes)));
+  return r;
+}
+__device__ __forceinline__ uint4 eight_codes(uint2 c) {
+  return make_uint4(e4m3_to_f16x2(c.x), e4m3_to_f16x2(c.x >> 16), e4m3_to_f16x2(c.y), e4m3_to_f16x2(c.y >> 16));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// bf16 pairs times a power of two as fp16.
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t x, float factor) {
+  const float2 f = unpack_bf16x2(x);
+  return pack_f16x2(f.x * factor, f.y * factor);
+}
+__device__ __forceinline__ uint4 scaled_f16(uint4 x, float factor) {
+  return make_uint4(bf16x2_to_f16x2(x.x, factor), bf16x2_to_f16x2(x.y, factor), bf16x2_to_f16x2(x.z, factor),
+                    bf16x2_to_f16x2(x.w, factor));
 }
 
-// Channels in the order that e4m3_pairs leaves them: (0, 2, 1, 3) of each four.
-__device__ __forceinline__ uint4 reorder(uint4 v) {
-  return make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632),
-                    __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.z, v.w, 0x7632));
+// Asynchronous TMEM load of 64 columns; the registers hold it after tmem_arrived.
+__device__ __forceinline__ void tmem_ld64_async(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+      : SALAD_R8(r, 0), SALAD_R8(r, 8), SALAD_R8(r, 16), SALAD_R8(r, 24), SALAD_R8(r, 32),
+        SALAD_R8(r, 40), SALAD_R8(r, 48), SALAD_R8(r, 56)
+      : "r"(taddr)
+      : "memory");
+}
+#define SALAD_RW8(a, o) "+r"(a[o + 0]), "+r"(a[o + 1]), "+r"(a[o + 2]), "+r"(a[o + 3]), \
+                        "+r"(a[o + 4]), "+r"(a[o + 5]), "+r"(a[o + 6]), "+r"(a[o + 7])
+// Waits for every load of this thread.
+__device__ __forceinline__ void tmem_arrived() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Keeps uses of r behind the wait before it.
+__device__ __forceinline__ void pin64(uint32_t* r) {
+  asm volatile("" : SALAD_RW8(r, 0), SALAD_RW8(r, 8));
+  asm volatile("" : SALAD_RW8(r, 16), SALAD_RW8(r, 24));
+  asm volatile("" : SALAD_RW8(r, 32), SALAD_RW8(r, 40));
+  asm volatile("" : SALAD_RW8(r, 48), SALAD_RW8(r, 56));
+}
+
+// Untiled bulk copy global -> shared completing on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// The power of two that brings magnitudes up to bf16 bits `top` (finite) to
+// at most 448: a closed block's rule.
+__device__ __forceinline__ float tail_scale(uint32_t top) {
+  int e = static_cast<int>(top >> 7) - 127 - 8 + ((top & 127u) > 96u ? 1 : 0);
+  e = e < -100 ? -100 : e;
+  return __int_as_float((127 + e) << 23);
 }
 
 __device__ __forceinline__ uint32_t finite_or_zero(uint32_t pair) {
@@ -263,7 +330,7 @@ __device__ __forceinline__ uint32_t finite_or_zero(uint32_t pair) {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_constant__ TcParams T) {
   using C = CT<D>;
-  constexpr int NS = C::kStages;
+  constexpr int NS = C::kStages, NR = C::kRaws;
   const CacheAttnParams& P = T.a;
   extern __shared__ __align__(1024) unsigned char smem[];
   if (reinterpret_cast<uintptr_t>(smem) & 1023u) {
@@ -277,39 +344,50 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
   if (w0 >= w1) return;
 
   unsigned char* qbuf = smem;                               // [2 slots][d-slab][128 rows]
-  unsigned char* ring = smem + 2 * C::kOperand;             // [NS][d-slab][128 rows]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + NS * C::kOperand);
-  // full[NS] empty[NS] q_full[2] q_free[2] s_full[2] p_full[2] o_done[2] drain
+  unsigned char* ring = qbuf + 2 * C::kOperand;             // [NS][d-slab][128 rows]
+  unsigned char* raws = ring + NS * C::kOperand;            // [NR][128 keys][d codes]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(raws + NR * C::kRaw);
+  // full[NS] empty[NS] raw_full[NR] raw_empty[NR] q_full[2] q_free[2] s_full[2] p_full[2] o_done[2] drain
   auto bar = [&](int i) { return smem_u32(bars + i); };
   auto full = [&](int i) { return bar(i); };
   auto empty = [&](int i) { return bar(NS + i); };
-  auto q_full = [&](int i) { return bar(2 * NS + i); };
-  auto q_free = [&](int i) { return bar(2 * NS + 2 + i); };
-  auto s_full = [&](int i) { return bar(2 * NS + 4 + i); };
-  auto p_full = [&](int i) { return bar(2 * NS + 6 + i); };
-  auto o_done = [&](int i) { return bar(2 * NS + 8 + i); };
-  const uint32_t drain = bar(2 * NS + 10);
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * NS + 11);
+  auto raw_full = [&](int i) { return bar(2 * NS + i); };
+  auto raw_empty = [&](int i) { return bar(2 * NS + NR + i); };
+  constexpr int B0 = 2 * NS + 2 * NR;
+  auto q_full = [&](int i) { return bar(B0 + i); };
+  auto q_free = [&](int i) { return bar(B0 + 2 + i); };
+  auto s_full = [&](int i) { return bar(B0 + 4 + i); };
+  auto p_full = [&](int i) { return bar(B0 + 6 + i); };
+  auto o_done = [&](int i) { return bar(B0 + 8 + i); };
+  const uint32_t drain = bar(B0 + 10);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + B0 + 11);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   // odd_seg[i % 4] = i + 1: part i's open block holds a value that is not finite.
   volatile int* odd_seg = abort_flag + 1;
-  static_assert((2 * NS + 11) * 8 + 4 + 4 + 16 <= C::kBarBytes, "barrier region");
+  static_assert((B0 + 11) * 8 + 4 + 4 + 16 <= C::kBarBytes, "barrier region");
   // Scales of tile i's two blocks in entry i % 4: of the keys (0: no page, its
-  // keys do not count), then of the values.  A converting thread writes them
-  // before it hands over the tile's keys.  It reaches tile i + 4 only when the
-  // values of tile i + 3 are stored, over those of tile i + 1: both slots have
-  // read tile i's scales by then.
+  // keys do not count), then of the values.  Warp 9 writes them with the bulk
+  // copy of the tile's keys, at the earliest when the keys of tile i - 2 are
+  // converted: over an operand tile whose MMAs waited for both slots' softmax
+  // of tile i - 4, so that entry has been read.
   float4* scales = reinterpret_cast<float4*>(reinterpret_cast<unsigned char*>(bars) + C::kBarBytes);
   // Tiles and slots of part i in entry i % 4, for the issuer: written and read
   // like the scales (a part has a tile at least).
   int2* part_info = reinterpret_cast<int2*>(scales + 4);
+  // A softmax warp's current part: registers hold a row of scores instead.
+  static_assert(sizeof(Seg) <= 64 && sizeof(Seg) % 4 == 0, "part record");
+  volatile int* seg_mem = reinterpret_cast<volatile int*>(part_info + 4) + 16 * (threadIdx.x / 32 % 8);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const unsigned long long wait_ns = P.wait_ns;
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(full(i), 4);      // the four converting warps
+      mbar_init(full(i), 3);      // the three converting warps
       mbar_init(empty(i), 1);
+    }
+    for (int i = 0; i < NR; ++i) {
+      mbar_init(raw_full(i), 1);
+      mbar_init(raw_empty(i), 3);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full(i), 4);    // the slot's four softmax warps
@@ -323,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
     for (int i = 0; i < 4; ++i) odd_seg[i] = 0;
     fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == 8) {
     tmem_alloc(smem_u32(tmem_holder), C::kCols);
     tmem_relinquish();
   }
@@ -332,23 +410,32 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
 
-  // Register shares, 4 x 128 in all: 160 for each softmax warpgroup, 128 for
-  // the converting one, 64 for the issuer's.
-  if (warp >= 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (warp == 12 && lane == 0) {
+  // Register shares, 3 x 168 in all: 192 for each softmax warpgroup, 120 for
+  // the other.
+  if (warp == 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+    if (lane == 0) {
       // ===================================================== MMA issuer
-      constexpr uint32_t idesc_qk = idesc_bf16(128, 128, false, false);
-      constexpr uint32_t idesc_pv = idesc_bf16(128, D, false, true);
+      constexpr uint32_t idesc_qk = idesc_f16(128, 128, false, false);
+      constexpr uint32_t idesc_pv = idesc_f16(128, D, false, true);
       const uint32_t ring_base = smem_u32(ring);
       const uint64_t qd[2] = {sdesc_sw128(smem_u32(qbuf), 16, 1024),
                               sdesc_sw128(smem_u32(qbuf) + C::kOperand, 16, 1024)};
-      uint32_t at = 0;                      // ring stages consumed so far
+      // Operand stage and phase of the next K or V, in the order K0 V0 K1 V1 ...
+      int st = 0;
+      uint32_t ph = 0;
       uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};
       bool ok = true;
-      auto wait_stage = [&](uint32_t i) -> bool { return mbar_wait(full(i % NS), (i / NS) & 1u, wait_ns, abort_flag); };
-      auto issue_qk = [&](int slot, uint32_t i) {
-        const uint64_t kd = sdesc_sw128(ring_base + (i % NS) * C::kOperand, 16, 1024);
+      auto wait_stage = [&]() -> bool { return mbar_wait(full(st), ph, wait_ns, abort_flag); };
+      auto next_stage = [&]() {
+        mma_commit(empty(st));
+        if (++st == NS) {
+          st = 0;
+          ph ^= 1u;
+        }
+      };
+      auto issue_qk = [&](int slot, int stage) {
+        const uint64_t kd = sdesc_sw128(ring_base + stage * C::kOperand, 16, 1024);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint64_t off = static_cast<uint64_t>(((ks / 4) * C::kRowSlab + (ks % 4) * 32) >> 4);
@@ -358,24 +445,25 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
       };
       int left = static_cast<int>(w1 - w0);
       for (int part_no = 0; left > 0 && ok; ++part_no) {
-        // Stages of the part: K0 V0 K1 V1 ...
-        if (!wait_stage(at)) { ok = false; break; }
+        if (!wait_stage()) { ok = false; break; }
         const int2 info = part_info[part_no % 4];
         const int n = info.x, slots = info.y;
         for (int slot = 0; slot < slots && ok; ++slot) {
           ok = mbar_wait(q_full(slot), qn[slot]++ & 1u, wait_ns, abort_flag);
           if (!ok) break;
           tc_fence_after();
-          issue_qk(slot, at);
+          issue_qk(slot, st);
           if (n == 1) mma_commit(q_free(slot));
         }
         if (!ok) break;
-        mma_commit(empty(at % NS));
+        next_stage();
         for (int t = 0; t < n && ok; ++t) {
-          const uint32_t vi = at + 2 * t + 1;
-          const uint64_t vd = sdesc_sw128(ring_base + (vi % NS) * C::kOperand, C::kRowSlab, 1024);
+          // V(t) in this stage, K(t + 1) in the next.
+          const uint64_t vd = sdesc_sw128(ring_base + st * C::kOperand, C::kRowSlab, 1024);
+          const int kst = st + 1 == NS ? 0 : st + 1;
+          const uint32_t kph = st + 1 == NS ? ph ^ 1u : ph;
           for (int slot = 0; slot < slots && ok; ++slot) {
-            ok = mbar_wait(p_full(slot), pn[slot]++ & 1u, wait_ns, abort_flag) && (slot > 0 || wait_stage(vi));
+            ok = mbar_wait(p_full(slot), pn[slot]++ & 1u, wait_ns, abort_flag) && (slot > 0 || wait_stage());
             if (!ok) break;
             tc_fence_after();
             const uint32_t sa = tmem + C::s_col(slot), oa = tmem + C::o_col(slot);
@@ -384,50 +472,41 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
               mma_ts(oa, sa + ks * 8, vd + static_cast<uint64_t>((ks * 2048) >> 4), idesc_pv,
                      ks > 0 ? 1u : (t > 0 ? 1u : 0u));
             mma_commit(o_done(slot));
-            if (slot == slots - 1) mma_commit(empty(vi % NS));
             if (t + 1 < n) {
-              if (slot == 0 && !wait_stage(vi + 1)) { ok = false; break; }
+              if (slot == 0 && !mbar_wait(full(kst), kph, wait_ns, abort_flag)) { ok = false; break; }
               tc_fence_after();
-              issue_qk(slot, vi + 1);            // over this slot's P: behind its PV in issue order
+              issue_qk(slot, kst);               // over this slot's P: behind its PV in issue order
               if (t + 2 == n) mma_commit(q_free(slot));
-              if (slot == slots - 1) mma_commit(empty((vi + 1) % NS));
             }
           }
+          if (!ok) break;
+          next_stage();
+          if (t + 1 < n) next_stage();
         }
-        at += 2 * n;
         left -= n;
       }
       if (!ok) raise_timeout(P.err, abort_flag);
       mma_commit(drain);
       if (!mbar_wait(drain, 0, wait_ns, nullptr)) atomicOr(P.err, kErrTimeout);
     }
-  } else if (warp >= 8) {
-    // ================================================== codes -> bf16
-    const int w = warp - 8;
-    const int c16 = lane % 4;                   // 16 channels of a 64-channel slab
-    const int r8 = 8 * w + lane / 4;            // rows r8 + 32 i; rows 64 and up are the tile's second block
-    uint32_t at = 0;                            // operand tiles written so far
-    int part_no = 0;
+  } else if (warp > 8) {
+    // ================================================== codes -> fp16
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+    const int w = warp - 9;
+    constexpr int CPR = D / 16;                 // 16-code chunks of a row
+    constexpr int RU = 32 / CPR;                // rows of one warp step
+    const int c = lane % CPR, rl = lane / CPR;
+    // Which eight codes of a lane's sixteen go first: chosen so that neither
+    // the 8-byte reads nor the swizzled 16-byte writes meet in a bank.
+    const int swap = D == 128 ? (c >> 2) ^ (rl & 1) : (rl >> 1) & 1;
     bool ok = true;
-    // Codes of one operand tile: rows i of block i / 2.
-    auto load = [&](uint4 (&to)[4][C::kSlabs], const unsigned char* pages, const int (&page)[2], int h) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int pg = page[i / 2];
-        const unsigned char* p =
-            pages + ((static_cast<long long>(pg < 0 ? 0 : pg) * P.c.H + h) * kCacheBlock + (r8 + 32 * i) % 64) * D + 16 * c16;
-#pragma unroll
-        for (int s = 0; s < C::kSlabs; ++s)
-          to[i][s] = pg == -2 ? make_uint4(0u, 0u, 0u, 0u) : __ldg(reinterpret_cast<const uint4*>(p + 64 * s));
-      }
-    };
-    // Pages and scales of 32 blocks, one per lane: -2 where the block is not
-    // closed.  A table entry that is no page reads page 0 with a key scale of
-    // 0, by which the softmax masks its keys.
-    struct Blocks {
-      int page;
+
+    // ---- warp 9: bulk copies, ahead of the conversion.
+    struct Blocks {                             // of 32 blocks, one per lane
+      int page;                                 // -2: not closed
       float ks, vs;
     };
+    // A table entry that is no page reads page 0; a key scale of 0 masks it.
     auto blocks_at = [&](const Seg& g, int blk) {
       Blocks k{-2, 1.0f, 1.0f};
       if (blk + lane < g.s.len / kCacheBlock) {
@@ -435,6 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
         if (k.page < 0) {
           k.page = 0;
           k.ks = 0.0f;
+          atomicOr(P.err, kErrRange);
         } else {
           const long long at = static_cast<long long>(k.page) * P.c.H + g.h;
           k.ks = __ldg(P.c.k_scale + at);
@@ -443,157 +523,264 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
       }
       return k;
     };
-    auto pages_of = [&](const Blocks& k, int i, int (&page)[2]) {
-      page[0] = __shfl_sync(0xffffffffu, k.page, 2 * i);
-      page[1] = __shfl_sync(0xffffffffu, k.page, 2 * i + 1);
+    // Scale of the open block's finite keys or values.
+    auto open_scale = [&](const Seg& g, const void* base) {
+      const uint4* tail = reinterpret_cast<const uint4*>(
+          static_cast<const __nv_bfloat16*>(base) +
+          ((static_cast<long long>(g.b) * 2 + g.s.slot) * P.c.H + g.h) * kCacheBlock * D);
+      const int n = g.s.len % kCacheBlock * (D / 8);
+      uint32_t top = 0;
+#pragma unroll 8
+      for (int e = lane; e < n; e += 32) {
+        const uint4 x = __ldg(tail + e);
+        top = __vmaxu2(top, finite_or_zero(x.x) & 0x7fff7fffu);
+        top = __vmaxu2(top, finite_or_zero(x.y) & 0x7fff7fffu);
+        top = __vmaxu2(top, finite_or_zero(x.z) & 0x7fff7fffu);
+        top = __vmaxu2(top, finite_or_zero(x.w) & 0x7fff7fffu);
+      }
+      return tail_scale(__reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16)));
     };
-    // The open block's rows over this thread's zeros of a tile, in bf16.  Values that are
-    // not finite would spread as 0 * inf; they are left to the rows that see
-    // them.  (Rolled up: the loop over closed tiles must stay in the
-    // instruction cache.)
-    auto store_open = [&](unsigned char* dst, const Seg& g, int half, bool value) {
-      const int held = g.s.len % kCacheBlock;
-      const __nv_bfloat16* tail = static_cast<const __nv_bfloat16*>(value ? P.c.v_tail : P.c.k_tail) +
-                                  ((static_cast<long long>(g.b) * 2 + g.s.slot) * P.c.H + g.h) * kCacheBlock * D;
-      bool odd = false;
-      // This thread's own rows and chunks of the half.
-#pragma unroll 1
-      for (int e = 0; e < 4 * C::kSlabs; ++e) {
-        const int row = r8 + 32 * (e & 1), c = 8 * (e >> 2) + 2 * c16 + ((e >> 1) & 1);
-        if (row >= held) continue;
-        uint4 x = reorder(__ldg(reinterpret_cast<const uint4*>(tail + row * D) + c));
-        if (value) {
-          const uint4 y = make_uint4(finite_or_zero(x.x), finite_or_zero(x.y), finite_or_zero(x.z), finite_or_zero(x.w));
-          odd = odd || y.x != x.x || y.y != x.y || y.z != x.z || y.w != x.w;
-          x = y;
+    Seg pg = seg_at(T, w0, w1 - w0);            // next operand tile to copy
+    int pt = pg.t0, p_part = 0;
+    bool p_value = false;
+    uint32_t p_at = 0, p_tile = 0;
+    Blocks cur{}, nxt{};
+    auto produce = [&]() -> bool {
+      if (pg.left <= 0) return true;
+      const int rs = static_cast<int>(p_at % NR);
+      const uint32_t n = p_at / NR;
+      if (n > 0 && !__all_sync(0xffffffffu, mbar_wait(raw_empty(rs), (n - 1) & 1u, wait_ns, abort_flag))) return false;
+      const int j = pg.all.first + pt, i = (pt - pg.t0) % 16;
+      if (!p_value) {
+        if (pt == pg.t0) nxt = blocks_at(pg, 2 * j);
+        if (i == 0) {
+          cur = nxt;
+          nxt = blocks_at(pg, 2 * j + 32);      // needed 16 tiles on
         }
-        const int at_row = 64 * half + row;
-        *reinterpret_cast<uint4*>(dst + (c / 8) * C::kRowSlab + at_row * 128 + (((c % 8) ^ (at_row & 7)) << 4)) = x;
-      }
-      if (odd) odd_seg[part_no % 4] = part_no + 1;
-    };
-    Seg g = seg_at(T, w0, w1 - w0);
-    uint32_t tile_no = 0;
-    // 16 tiles' blocks, and the 16 after them (loaded 16 tiles early).
-    Blocks cur = blocks_at(g, 2 * (g.all.first + g.t0)), nxt = cur;
-    int page[2];
-    pages_of(cur, 0, page);
-    uint4 raw[4][C::kSlabs];
-    load(raw, P.c.k_pages, page, g.h);
-    // One operand tile a turn, K and V of a tile after one another; the next
-    // one's loads are in flight while this one is converted.
-    int t = g.t0;
-    bool value = false, more = true;
-#pragma unroll 1
-    while (more && ok) {
-      const int j = g.all.first + t, i = (t - g.t0) % 16;
-      const int open = g.s.len / kCacheBlock - 2 * j;    // 0 or 1: the open block is that half
-      Seg ng = g;
-      int nt = t;
-      uint4 ahead[4][C::kSlabs];
-      if (!value) {
-        if (i == 0) nxt = blocks_at(g, 2 * j + 32);
-        const float k0 = __shfl_sync(0xffffffffu, cur.ks, 2 * i), k1 = __shfl_sync(0xffffffffu, cur.ks, 2 * i + 1);
-        const float v0 = __shfl_sync(0xffffffffu, cur.vs, 2 * i), v1 = __shfl_sync(0xffffffffu, cur.vs, 2 * i + 1);
-        if (w == 0 && lane == 0) {
-          if (t == g.t0) part_info[part_no % 4] = make_int2(g.t1 - g.t0, g.two ? 2 : 1);
-          scales[tile_no % 4] = make_float4(k0, k1, v0, v1);
-          if (k0 == 0.0f || k1 == 0.0f) atomicOr(P.err, kErrRange);
+        float4 sc = make_float4(__shfl_sync(0xffffffffu, cur.ks, 2 * i), __shfl_sync(0xffffffffu, cur.ks, 2 * i + 1),
+                                __shfl_sync(0xffffffffu, cur.vs, 2 * i), __shfl_sync(0xffffffffu, cur.vs, 2 * i + 1));
+        const int open = pg.s.len / kCacheBlock - 2 * j;
+        if (open == 0 || open == 1) {
+          const float ks = open_scale(pg, P.c.k_tail), vs = open_scale(pg, P.c.v_tail);
+          (open ? sc.y : sc.x) = ks;
+          (open ? sc.w : sc.z) = vs;
         }
-      } else {
-        ++nt;
-        if (nt == g.t1) {
-          ng = seg_next(P, g);
-          more = ng.left > 0;
-          nt = ng.t0;
-          if (more) cur = blocks_at(ng, 2 * (ng.all.first + nt));
-          pages_of(cur, 0, page);
-        } else {
-          if (i == 15) cur = nxt;
-          pages_of(cur, (i + 1) % 16, page);
+        if (lane == 0) {
+          if (pt == pg.t0) part_info[p_part % 4] = make_int2(pg.t1 - pg.t0, pg.two ? 2 : 1);
+          scales[p_tile % 4] = sc;
         }
       }
-      if (more) load(ahead, value ? P.c.k_pages : P.c.v_pages, page, ng.h);
-      // Store this one, once the MMAs that read its stage have run.
-      const int st = static_cast<int>(at % NS);
-      const uint32_t n = at / NS;
-      if (n > 0 && !__all_sync(0xffffffffu, mbar_wait(empty(st), (n - 1) & 1u, wait_ns, abort_flag))) {
-        ok = false;
-        break;
+      const int p0 = __shfl_sync(0xffffffffu, cur.page, 2 * i), p1 = __shfl_sync(0xffffffffu, cur.page, 2 * i + 1);
+      if (lane == 0) {
+        constexpr uint32_t bytes = kCacheBlock * D;
+        const unsigned char* pages = p_value ? P.c.v_pages : P.c.k_pages;
+        const uint32_t dst = smem_u32(raws) + rs * C::kRaw;
+        mbar_arrive_expect_tx(raw_full(rs), (p0 >= 0 ? bytes : 0u) + (p1 >= 0 ? bytes : 0u));
+        if (p0 >= 0) bulk_load(dst, pages + (static_cast<long long>(p0) * P.c.H + pg.h) * bytes, bytes, raw_full(rs));
+        if (p1 >= 0) bulk_load(dst + bytes, pages + (static_cast<long long>(p1) * P.c.H + pg.h) * bytes, bytes, raw_full(rs));
       }
-      unsigned char* dst = ring + st * C::kOperand;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int row = r8 + 32 * x;
-#pragma unroll
-        for (int s = 0; s < C::kSlabs; ++s) {
-          uint4 lo, hi;
-          e4m3_pairs(raw[x][s].x, lo.x, lo.y);
-          e4m3_pairs(raw[x][s].y, lo.z, lo.w);
-          e4m3_pairs(raw[x][s].z, hi.x, hi.y);
-          e4m3_pairs(raw[x][s].w, hi.z, hi.w);
-          unsigned char* to = dst + s * C::kRowSlab + row * 128;
-          *reinterpret_cast<uint4*>(to + (((2 * c16) ^ (row & 7)) << 4)) = lo;
-          *reinterpret_cast<uint4*>(to + (((2 * c16 + 1) ^ (row & 7)) << 4)) = hi;
-        }
-      }
-      if (open == 0 || open == 1) store_open(dst, g, open, value);
-      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(full(st));
-      ++at;
-      if (value) {
-        ++tile_no;
-        if (t + 1 == g.t1) ++part_no;
-        g = ng;
-        t = nt;
+      ++p_at;
+      if (p_value) {
+        ++p_tile;
+        if (++pt == pg.t1) {
+          pg = seg_next(P, pg);
+          pt = pg.t0;
+          ++p_part;
+        }
       }
-      value = !value;
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-#pragma unroll
-        for (int s = 0; s < C::kSlabs; ++s) raw[x][s] = ahead[x][s];
+      p_value = !p_value;
+      return true;
+    };
+    if (w == 0)
+      for (int i = 0; i < NR && ok; ++i) ok = produce();
+
+    // ---- conversion, operand tile by operand tile
+    Seg g = seg_at(T, w0, w1 - w0);
+    int part_no = 0;
+    uint32_t tile_no = 0;
+    int st = 0, rs = 0;
+    uint32_t sph = 1, rph = 0;                  // parities of empty (first turn passes) and raw_full
+    while (g.left > 0 && ok) {
+#pragma unroll 1
+      for (int o = 2 * g.t0; o < 2 * g.t1 && ok; ++o) {
+        const bool value = o & 1;
+        const int j = g.all.first + (o >> 1);
+        const int closed = g.s.len / kCacheBlock - 2 * j;   // of the tile's blocks: 2 and more, 1, 0 and less
+        if (!__all_sync(0xffffffffu, mbar_wait(raw_full(rs), rph, wait_ns, abort_flag) &&
+                                         mbar_wait(empty(st), sph, wait_ns, abort_flag))) {
+          ok = false;
+          break;
+        }
+        const unsigned char* src = raws + rs * C::kRaw;
+        unsigned char* dst = ring + st * C::kOperand;
+        const float4 sc = scales[tile_no % 4];
+        // Value blocks of NaN, or of no page, are left out here (their codes
+        // may be NaN; the softmax marks the rows that see them).
+        const bool out0 = value && (isnan(sc.z) || sc.x == 0.0f), out1 = value && (isnan(sc.w) || sc.y == 0.0f);
+        const int first = closed >= 1 && !out0 ? 0 : 64, last = closed >= 2 && !out1 ? 128 : 64;
+#pragma unroll 4
+        for (int r0 = first + w * RU; r0 < last; r0 += 3 * RU) {
+          const int row = r0 + rl;
+          const unsigned char* from = src + row * D + 16 * c;
+          const uint2 a = *reinterpret_cast<const uint2*>(from + 8 * swap);
+          const uint2 b = *reinterpret_cast<const uint2*>(from + 8 * (swap ^ 1));
+          unsigned char* to = dst + (c / 4) * C::kRowSlab + row * 128;
+          const int ch = (2 * c) & 7;
+          *reinterpret_cast<uint4*>(to + (((ch + swap) ^ (row & 7)) << 4)) = eight_codes(a);
+          *reinterpret_cast<uint4*>(to + (((ch + (swap ^ 1)) ^ (row & 7)) << 4)) = eight_codes(b);
+        }
+        if (last - first < 128) {
+          // The open block's rows, scaled, and zeros elsewhere.  Values that
+          // are not finite would spread as 0 * inf; they are left to the rows
+          // that see them.
+          const float inv = pow2_inv(value ? (closed == 1 ? sc.w : sc.z) : (closed == 1 ? sc.y : sc.x));
+          const uint4* tail = reinterpret_cast<const uint4*>(
+              static_cast<const __nv_bfloat16*>(value ? P.c.v_tail : P.c.k_tail) +
+              ((static_cast<long long>(g.b) * 2 + g.s.slot) * P.c.H + g.h) * kCacheBlock * D);
+          const int open = closed == 0 || closed == 1 ? 64 * closed : 128;   // the open block's first row
+          const int held = g.s.len % kCacheBlock;
+          bool odd = false;
+#pragma unroll 1
+          for (int e = w * 32 + lane; e < 128 * (D / 8); e += 96) {
+            const int row = e / (D / 8), ch = e % (D / 8);
+            if (row >= first && row < last) continue;
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            if (row >= open && row - open < held) {
+              x = __ldg(tail + (row - open) * (D / 8) + ch);
+              if (value) {
+                const uint4 y = make_uint4(finite_or_zero(x.x), finite_or_zero(x.y), finite_or_zero(x.z), finite_or_zero(x.w));
+                odd = odd || y.x != x.x || y.y != x.y || y.z != x.z || y.w != x.w;
+                x = y;
+              }
+              x = scaled_f16(x, inv);
+            }
+            *reinterpret_cast<uint4*>(dst + (ch / 8) * C::kRowSlab + row * 128 + (((ch % 8) ^ (row & 7)) << 4)) = x;
+          }
+          if (odd) odd_seg[part_no % 4] = part_no + 1;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(full(st));
+          mbar_arrive(raw_empty(rs));
+        }
+        if (++st == NS) {
+          st = 0;
+          sph ^= 1u;
+        }
+        if (++rs == NR) {
+          rs = 0;
+          rph ^= 1u;
+        }
+        if (value) ++tile_no;
+        if (w == 0) ok = produce();
+      }
+      ++part_no;
+      g = seg_next(P, g);
     }
     if (!ok) raise_timeout(P.err, abort_flag);
+    // No bulk copy may be in flight at the exit.
+    if (w == 0 && lane == 0) {
+      for (uint32_t i = 0; i < NR && i < p_at; ++i) {
+        const uint32_t last = (p_at - 1 - i) / NR;          // turns of raw slot i, less one
+        if (!mbar_wait(raw_full(static_cast<int>(i)), last & 1u, wait_ns, nullptr)) atomicOr(P.err, kErrTimeout);
+      }
+    }
   } else {
     // ============================================ softmax and output
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     const int slot = warp / 4, quarter = warp % 4;
     const int r = quarter * 32 + lane;                  // row of the slot (TMEM lane)
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t sbuf = lane_base + C::s_col(slot), obuf = lane_base + C::o_col(slot);
     uint32_t sn = 0, on = 0, parts = 0;                 // S tiles, PVs and parts of this slot so far
     bool ok = true;
-    // This slot's rows of a part's Q into shared memory (zeros where there is no row).
-    auto load_q = [&](const Seg& g) {
+    // This slot's rows of a part's Q into shared memory (zeros where there is
+    // no row), scaled; returns what the row's scores are to be multiplied by.
+    auto load_q = [&](const Seg& g) -> float {
       const CacheRow row = cache_row(P, g.tile * kRows + slot * 128 + r, g.h, g.s.len, g.s.count);
       const uint4* from = reinterpret_cast<const uint4*>(P.q + g.b * P.qb + row.head * P.qh + row.n * P.qn);
       unsigned char* to = qbuf + slot * C::kOperand + r * 128;
+      uint4 x[D / 8];
+      uint32_t top = 0;
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 v = row.valid ? from[c] : make_uint4(0u, 0u, 0u, 0u);
-        *reinterpret_cast<uint4*>(to + (c / 8) * C::kRowSlab + (((c % 8) ^ (r & 7)) << 4)) = reorder(v);
+      for (int i = 0; i < D / 8; ++i) {
+        x[i] = row.valid ? from[i] : make_uint4(0u, 0u, 0u, 0u);
+        top = __vmaxu2(__vmaxu2(top, x[i].x & 0x7fff7fffu), x[i].y & 0x7fff7fffu);
+        top = __vmaxu2(__vmaxu2(top, x[i].z & 0x7fff7fffu), x[i].w & 0x7fff7fffu);
       }
+      top = max(top & 0xffffu, top >> 16);
+      // A row with an infinity or a NaN stays as it is.
+      int e = top >= 0x7f80u ? 0 : static_cast<int>(top >> 7) - 127 - 14;
+      e = e < -100 ? -100 : e;
+      const float down = __int_as_float((127 - e) << 23);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+        *reinterpret_cast<uint4*>(to + (i / 8) * C::kRowSlab + (((i % 8) ^ (r & 7)) << 4)) = scaled_f16(x[i], down);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full(slot));
+      return __int_as_float((127 + e) << 23);
     };
-    uint32_t tile_no = 0;                               // of the CTA
-    Seg g = seg_at(T, w0, w1 - w0);
+    auto keep_seg = [&](const Seg& g) {
+      int x[sizeof(Seg) / 4];
+      memcpy(x, &g, sizeof(Seg));
+      __syncwarp();
+      if (lane == 0)
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(Seg) / 4); ++i) seg_mem[i] = x[i];
+      __syncwarp();
+    };
+    auto kept_seg = [&]() {
+      Seg g;
+      int x[sizeof(Seg) / 4];
+#pragma unroll
+      for (int i = 0; i < static_cast<int>(sizeof(Seg) / 4); ++i) x[i] = seg_mem[i];
+      memcpy(&g, x, sizeof(Seg));
+      return g;
+    };
+    auto row_of = [&](const Seg& g) {
+      return cache_row(P, g.tile * kRows + slot * 128 + r, g.h, g.s.len, g.s.count);
+    };
     int part_no = 0;
+    uint32_t tile_no = 0;                               // of the CTA
+    bool more, mine;
     // A slot without rows takes no part in an item; the next item of the CTA
     // may have some again.
-    if (slot == 0 || g.two) load_q(g);
-    while (g.left > 0 && ok) {
-      const Seg ng = seg_next(P, g);
-      const bool mine = slot == 0 || g.two;
+    float q_factor = 1.0f;
+    auto start = [&](const Seg& g) {
+      more = g.left > 0;
+      mine = more && (slot == 0 || g.two);
+      if (mine) q_factor = load_q(g);
+    };
+    {
+      const Seg g = seg_at(T, w0, w1 - w0);
+      keep_seg(g);
+      start(g);
+    }
+    while (more && ok) {
+      int j0, n, all_lo, all_end;
+      {
+        const Seg g = kept_seg();
+        j0 = g.all.first + g.t0;
+        n = g.t1 - g.t0;
+        const CacheRow row = row_of(g);
+        // Keys that every row of the warp sees.
+        all_lo = __reduce_max_sync(0xffffffffu, row.valid ? row.see.lo : 0);
+        all_end = __reduce_min_sync(0xffffffffu, row.valid ? row.see.end : 0x7fffffff);
+      }
       if (mine) {
-        const CacheRow row = cache_row(P, g.tile * kRows + slot * 128 + r, g.h, g.s.len, g.s.count);
-        const int n = g.t1 - g.t0;
-        float m = -INFINITY, l = 0.0f;
+        const float c1 = P.scale_log2 * q_factor;
+        // P = 2^(s + ev - mt), ev the exponent of the value block's scale and
+        // mt the row's largest s + ev (raised lazily, by more than 2^8 at a
+        // time): what a block adds to O is then rounded against the largest
+        // such product, however the scales differ.  The row sum l is kept
+        // against the largest score, ms.
+        float mt = -INFINITY, ms = -INFINITY, l = 0.0f;
+        float ev_top = -INFINITY;                       // largest ev so far
         bool vbad = false;
         for (int t = 0; t < n; ++t) {
-          const int j = g.all.first + g.t0 + t;
           if (!__all_sync(0xffffffffu, mbar_wait(s_full(slot), sn & 1u, wait_ns, abort_flag))) {
             ok = false;
             break;
@@ -601,91 +788,98 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
           ++sn;
           tc_fence_after();
           const float4 sc = scales[(tile_no + t) % 4];
+          const int kb = (j0 + t) * kTile;
           // Halves outside some row's range: scores there become -inf, in
-          // TMEM.  (A NaN key scale makes the scores that are seen NaN.)  The
-          // halves' loops are rolled up: the code of a whole tile, beside
-          // the converting warps', must stay in the instruction cache.
-          uint32_t any = 0;
+          // TMEM.  (A NaN key scale makes the scores that are seen NaN; a NaN
+          // value scale marks the rows that see its block.)
+          const bool full0 = sc.x > 0.0f && !isnan(sc.z) && kb >= all_lo && kb + 64 <= all_end;
+          const bool full1 = sc.y > 0.0f && !isnan(sc.w) && kb + 64 >= all_lo && kb + 128 <= all_end;
+          if (!(full0 && full1)) {
+            const CacheSpan see = row_of(kept_seg()).see;
+            vbad = vbad || (isnan(sc.z) && max(see.lo, kb) < min(see.end, kb + 64)) ||
+                   (isnan(sc.w) && max(see.lo, kb + 64) < min(see.end, kb + 128));
 #pragma unroll 1
-          for (int x = 0; x < 2; ++x) {
-            const int kb = j * kTile + 64 * x;
-            const float ks = x ? sc.y : sc.x, vs = x ? sc.w : sc.z;
-            const int lo = row.see.lo - kb, hi = ks == 0.0f ? -1 : row.see.end - 1 - kb;
-            const bool live = lo < 64 && hi >= 0 && row.see.end > 0;
-            vbad = vbad || (live && isnan(vs));
-            if (!__any_sync(0xffffffffu, live)) continue;
-            any |= 1u << x;
-            if (!isnan(ks) && __all_sync(0xffffffffu, live && lo <= 0 && hi >= 63)) continue;
-            const float seen = isnan(ks) ? ks : 0.0f;
-#pragma unroll 1
-            for (int c0 = 0; c0 < 64; c0 += 32) {
+            for (int c0 = 0; c0 < 128; c0 += 32) {
+              const float ks = c0 < 64 ? sc.x : sc.y;
+              const int lo = see.lo - kb - c0, hi = ks == 0.0f ? -1 : see.end - 1 - kb - c0;
+              const float seen = isnan(ks) ? ks : 0.0f;
               uint32_t s32[32];
-              tmem_ld32(sbuf + 64 * x + c0, s32);
+              tmem_ld32(sbuf + c0, s32);
 #pragma unroll
               for (int c = 0; c < 32; ++c)
-                s32[c] = live && c0 + c >= lo && c0 + c <= hi ? __float_as_uint(__uint_as_float(s32[c]) + seen) : 0xff800000u;
-              tmem_st32(sbuf + 64 * x + c0, s32);
+                s32[c] = c >= lo && c <= hi ? __float_as_uint(__uint_as_float(s32[c]) + seen) : 0xff800000u;
+              tmem_st32(sbuf + c0, s32);
             }
             tmem_st_wait();
           }
-          // Pass 1: the row's maximum.
-          float pm = -INFINITY;
-#pragma unroll 1
-          for (int x = 0; x < 2; ++x) {
-            if (!(any >> x & 1u)) continue;
-            uint32_t s64[64];
-            tmem_ld64(sbuf + 64 * x, s64);
-            float sv[64];
-#pragma unroll
-            for (int c = 0; c < 64; ++c) sv[c] = __uint_as_float(s64[c]);
-            pm = fmaxf(pm, max64(sv) * key_factor(P.scale_log2, x ? sc.y : sc.x));
-          }
-          // The maximum is raised lazily: O is rescaled only when it grows by
-          // more than 2^8 (by anything under scales so large that P times 2^8
-          // would leave float32).
+          // The tile's scores of this row, in registers.
+          uint32_t sv[128];
+          tmem_ld64_async(sbuf, sv);
+          tmem_arrived();
+          tmem_ld64_async(sbuf + 64, sv + 64);          // travels while the first half is reduced
+          pin64(sv);
+          const float c20 = isnan(sc.x) ? 1.0f : fmaxf(c1 * sc.x, 1e-37f);   // positive: -inf stays -inf
+          const float c21 = isnan(sc.y) ? 1.0f : fmaxf(c1 * sc.y, 1e-37f);
+          const float ev0 = isnan(sc.z) ? 0.0f : pow2_log(sc.z), ev1 = isnan(sc.w) ? 0.0f : pow2_log(sc.w);
+          ev_top = fmaxf(ev_top, fmaxf(ev0, ev1));
+          const float s0 = max64(sv) * c20;
+          tmem_arrived();
+          pin64(sv + 64);
+          const float s1 = max64(sv + 64) * c21;
+          const float pm = fmaxf(s0 + ev0, s1 + ev1);
           float f = 1.0f;
-          const float slack = fmaxf(sc.z, sc.w) > 0x1p100f ? 0.0f : 8.0f;
-          if (pm > m + slack) {
-            f = m == -INFINITY ? 1.0f : ex2_ftz(m - pm);
-            l *= f;
-            m = pm;
+          if (pm > mt + 8.0f) {
+            f = mt == -INFINITY ? 1.0f : ex2_ftz(mt - pm);
+            mt = pm;
           }
-          const float nm = m == -INFINITY ? 0.0f : -m;
-          // Pass 2: P = 2^(s c2 - m + ev) over the first 64 columns of S.
-#pragma unroll 1
-          for (int x = 0; x < 2; ++x) {
-            uint32_t pk[32];
-            if (any >> x & 1u) {
-              const float vs0 = x ? sc.w : sc.z;
-              const float vs = isnan(vs0) ? 1.0f : vs0;
-              const float c2 = key_factor(P.scale_log2, x ? sc.y : sc.x);
-              const uint64_t c22 = pack2(c2, c2), off = pack2(nm + pow2_log(vs), nm + pow2_log(vs));
-              uint32_t s64[64];
-              tmem_ld64(sbuf + 64 * x, s64);
-              uint64_t a0 = 0, a1 = 0;
+          const float top = fmaxf(ms, fmaxf(s0, s1));
+          if (top > ms) {
+            l *= ex2_ftz(ms - top);
+            ms = top;
+          }
+          // A row that has seen no key: exp2(-inf - 0) = 0.
+          const float nm = mt == -INFINITY ? 0.0f : -mt, ns = ms == -INFINITY ? 0.0f : -ms;
+          float add = 0.0f;
 #pragma unroll
-              for (int c = 0; c < 64; c += 4) {
+          for (int x = 0; x < 2; ++x) {
+            const float c2 = x ? c21 : c20, ev = x ? ev1 : ev0;
+            const uint64_t c22 = pack2(c2, c2), off = pack2(nm + ev, nm + ev);
+            uint64_t a0 = 0, a1 = 0;
+            if (ev_top - ev > 90.0f) {
+              // P may vanish beside another block's; the sum must not.
+#pragma unroll 1
+              for (int c0 = 0; c0 < 64; c0 += 32) {
+                uint32_t s32[32];
+                tmem_ld32(sbuf + 64 * x + c0, s32);
+#pragma unroll
+                for (int c = 0; c < 32; ++c) add += ex2_ftz(fmaf(__uint_as_float(s32[c]), c2, ns));
+              }
+            }
+#pragma unroll
+            for (int c0 = 0; c0 < 64; c0 += 32) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int c = 0; c < 32; c += 4) {
+                const uint32_t* v = sv + 64 * x + c0 + c;
                 float p0, p1, p2, p3;
-                unpack2(fma2(pack2(__uint_as_float(s64[c]), __uint_as_float(s64[c + 1])), c22, off), p0, p1);
-                unpack2(fma2(pack2(__uint_as_float(s64[c + 2]), __uint_as_float(s64[c + 3])), c22, off), p2, p3);
+                unpack2(fma2(pack2(__uint_as_float(v[0]), __uint_as_float(v[1])), c22, off), p0, p1);
+                unpack2(fma2(pack2(__uint_as_float(v[2]), __uint_as_float(v[3])), c22, off), p2, p3);
                 p0 = ex2_ftz(p0);
                 p1 = ex2_ftz(p1);
                 p2 = ex2_ftz(p2);
                 p3 = ex2_ftz(p3);
-                pk[c / 2] = pack_bf16x2(p0, p1);
-                pk[c / 2 + 1] = pack_bf16x2(p2, p3);
+                pk[c / 2] = pack_f16x2(p0, p1);
+                pk[c / 2 + 1] = pack_f16x2(p2, p3);
                 a0 = add2(a0, pack2(p0, p1));
                 a1 = add2(a1, pack2(p2, p3));
               }
-              float s0, s1;
-              unpack2(add2(a0, a1), s0, s1);
-              l = fmaf(s0 + s1, pow2_inv(vs), l);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) pk[e] = 0u;
+              tmem_st16(sbuf + 32 * x + c0 / 2, pk);
             }
-            tmem_st32(sbuf + 32 * x, pk);
+            float u0, u1;
+            unpack2(add2(a0, a1), u0, u1);
+            if (!(ev_top - ev > 90.0f)) add = fmaf(u0 + u1, ex2_ftz(ns - nm - ev), add);
           }
+          l += add;
           // Every PV of the slot is observed in order: a parity wait is at
           // most one phase behind.
           if (t > 0) {
@@ -695,15 +889,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
             }
             ++on;
             tc_fence_after();
-          }
-          if (t > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
+            if (__any_sync(0xffffffffu, f != 1.0f)) {
 #pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 32) {
-              uint32_t o32[32];
-              tmem_ld32(obuf + c0, o32);
+              for (int c0 = 0; c0 < D; c0 += 32) {
+                uint32_t o32[32];
+                tmem_ld32(obuf + c0, o32);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o32[e] = __float_as_uint(__uint_as_float(o32[e]) * f);
-              tmem_st32(obuf + c0, o32);
+                for (int e = 0; e < 32; ++e) o32[e] = __float_as_uint(__uint_as_float(o32[e]) * f);
+                tmem_st32(obuf + c0, o32);
+              }
             }
           }
           tmem_st_wait();
@@ -718,16 +912,21 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
           break;
         }
         ++parts;
-        if (ng.left > 0 && (slot == 0 || ng.two)) load_q(ng);
+        const Seg g = kept_seg();
+        const CacheRow row = row_of(g);
+        const Seg ng = seg_next(P, g);
+        keep_seg(ng);
+        start(ng);
         if (!__all_sync(0xffffffffu, mbar_wait(o_done(slot), on & 1u, wait_ns, abort_flag))) {
           ok = false;
           break;
         }
         ++on;
         tc_fence_after();
-        // ---- output
+        // ---- output: O is in units of 2^mt, the sum of 2^ms
         const bool whole = g.t0 == 0 && g.t1 == g.all.n;
         const bool odd = odd_seg[part_no % 4] == part_no + 1;
+        const float unit = mt == -INFINITY ? 1.0f : ex2_ftz(mt - ms);
         const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
         char* orow = P.o + g.b * P.ob + row.head * P.oh + row.n * P.on;
         const long long part_row = (2ll * blockIdx.x + (g.first ? 0 : 1)) * kRows + slot * 128 + r;
@@ -737,11 +936,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
           tmem_ld32(obuf + c0, o32);
           float v[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            // Back to the channels' order.
-            const int from = (e & ~3) | ((e & 1) << 1) | ((e & 2) >> 1);
-            v[e] = vbad ? __int_as_float(0x7fffffff) : __uint_as_float(o32[from]);
-          }
+          for (int e = 0; e < 32; ++e) v[e] = vbad ? __int_as_float(0x7fffffff) : __uint_as_float(o32[e]) * unit;
           if (odd && row.valid) {
             const int first = g.s.len / kCacheBlock * kCacheBlock;
             const __nv_bfloat16* tail = static_cast<const __nv_bfloat16*>(P.c.v_tail) +
@@ -766,16 +961,17 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
           }
         }
         if (row.valid && whole && P.lse != nullptr)
-          P.lse[(static_cast<long long>(g.b) * P.Hq + row.head) * P.N + row.n] = (m + log2f(l)) * 0.6931471805599453f;
-        if (row.valid && !whole) P.part_ml[part_row] = make_float2(m, l);
+          P.lse[(static_cast<long long>(g.b) * P.Hq + row.head) * P.N + row.n] = (ms + log2f(l)) * 0.6931471805599453f;
+        if (row.valid && !whole) P.part_ml[part_row] = make_float2(ms, l);
         tc_fence_before();
-      } else if (ng.left > 0 && ng.two) {
+      } else {
         // No rows in this item: its slot's Q buffer is idle.
-        load_q(ng);
+        const Seg ng = seg_next(P, kept_seg());
+        keep_seg(ng);
+        start(ng);
       }
-      tile_no += g.t1 - g.t0;
+      tile_no += n;
       ++part_no;
-      g = ng;
     }
     if (!ok) raise_timeout(P.err, abort_flag);
     // No TMEM access of this warp may be in flight at the teardown.
@@ -784,7 +980,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kCols);
   }

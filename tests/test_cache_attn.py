@@ -5,9 +5,14 @@ Tolerances.  Scores are sums of d exact bf16 products in float32: off by at
 most D = d 2^-22 * scale * max_j sum_c |q_c k_jc| (2^-22 allows for the tensor
 core's truncated additions), which moves every weight by a factor within 1 +-
 D, so the output by at most 2 D A, where A = sum_j p_j |v_j| / sum_j p_j.  P is
-rounded to bf16 (2^-8 of each weight, so 2^-8 A), the sums of weights and of
-products are float32 (n 2^-23 A each for n keys; n <= 2200 here), and the
-output is rounded to bf16 (2^-8 |o|).  lse moves by D and n 2^-23.
+rounded to bf16 (2^-8 of each weight, so 2^-8 A) by the kernel of few rows.
+The one of many rows multiplies c_j = v_j / s_j, s_j the power-of-two scale of
+the key's block, by P_j = p_j s_j / max_i(p_i s_i), rounded to fp16: by 2^-11
+of it, or by half of fp16's smallest step, 2^-25, where that is more.  The
+latter adds at most F = 2^-25 max_i(p_i s_i) sum_j |c_j| / sum_j p_j.  The sums
+of weights and of products are float32 (n 2^-23 A each for n keys; n <= 2200
+here), and the output is rounded to bf16 (2^-8 |o|).  lse moves by D and
+n 2^-23.
 """
 import ctypes
 import math
@@ -97,8 +102,15 @@ def _make(B, H, d, lens, blocks=None, seed=0, extra=3):
     return cache, torch.stack([torch.tensor(lens), slots], 1).to(torch.int32).cuda()
 
 
+def _tail_scale(x):
+    """The scale of an open block's rows [H, n, d]: that of a closed block."""
+    top = torch.where(torch.isfinite(x), x.abs(), torch.zeros_like(x)).amax(dim=(1, 2))
+    part, e = torch.frexp(top / 448.0)
+    return torch.ldexp(torch.ones_like(top), (e - (part == 0.5).int()).clamp(min=-100))
+
+
 def _held(cache, seq, b):
-    """Keys and values of sequence b as float64 [H, len, d]."""
+    """Keys and values of sequence b as float64 [H, len, d], and the values' scales [H, len]."""
     n, slot = (int(x) for x in seq[b].cpu())
     out = []
     pages = cache.page_table[b, :n // 64].long().cpu()
@@ -106,18 +118,22 @@ def _held(cache, seq, b):
         x = getattr(cache, name + "_pages").cpu().double()[pages] * getattr(cache, name + "_scale").cpu().double()[pages][..., None, None]
         x = x.transpose(0, 1).reshape(cache.H, -1, cache.d)
         out.append(torch.cat([x, getattr(cache, name + "_tail").cpu().double()[b, slot, :, :n % 64]], 1))
-    return out
+    scale = cache.v_scale.cpu().double()[pages].T.repeat_interleave(64, 1)
+    if n % 64:
+        scale = torch.cat([scale, _tail_scale(out[1][:, n - n % 64:])[:, None].expand(-1, n % 64)], 1)
+    return out[0], out[1], scale
 
 
 def _reference(cache, q, seq, counts=None, frame=0, window=-1, scale=None):
     B, Hq, N, d = q.shape
     scale = 1 / math.sqrt(d) if scale is None else scale
     o = torch.zeros(B, Hq, N, d, dtype=torch.float64)
-    mean_abs, spread = torch.zeros_like(o), torch.zeros(B, Hq, N, 1, dtype=torch.float64)
+    mean_abs, flush = torch.zeros_like(o), torch.zeros_like(o)
+    spread = torch.zeros(B, Hq, N, 1, dtype=torch.float64)
     lse = torch.full((B, Hq, N), -math.inf, dtype=torch.float64)
     q64 = q.cpu().double()
     for b in range(B):
-        k, v = _held(cache, seq, b)
+        k, v, vs = _held(cache, seq, b)
         L, n = k.shape[1], N if counts is None else counts[b]
         for h in range(Hq):
             kh, vh = k[h // (Hq // cache.H)], v[h // (Hq // cache.H)]
@@ -134,7 +150,9 @@ def _reference(cache, q, seq, counts=None, frame=0, window=-1, scale=None):
                 lse[b, h, i] = torch.logsumexp(x, 0)
                 o[b, h, i] = w @ vh[lo:end]
                 mean_abs[b, h, i] = w @ vh[lo:end].abs()
-    return o, lse, mean_abs, spread
+                sc = vs[h // (Hq // cache.H), lo:end]
+                flush[b, h, i] = 2.0 ** -25 * (w * sc).max() * (vh[lo:end].abs() / sc[:, None]).sum(0)
+    return o, lse, mean_abs, flush, spread
 
 
 def _check(cache, q, seq, counts=None, **kw):
@@ -145,7 +163,7 @@ def _check(cache, q, seq, counts=None, **kw):
     got = salad.cache_attn(cache, q, seq, counts=c, o=o, lse=lse, **kw)
     assert got is o
     salad.check_error()
-    want, wlse, mean_abs, spread = _reference(cache, q, seq, counts, **kw)
+    want, wlse, mean_abs, flush, spread = _reference(cache, q, seq, counts, **kw)
     o, lse = o.cpu().double(), lse.cpu().double()
     D = d * 2.0 ** -22 * spread
     n = int(seq[:, 0].max()) * 2.0 ** -23
@@ -153,7 +171,7 @@ def _check(cache, q, seq, counts=None, **kw):
         m = N if counts is None else counts[b]
         assert torch.all(o[b, :, m:] == 5.0) and torch.all(lse[b, :, m:] == 5.0)     # rows behind a count
         err = (o[b, :, :m] - want[b, :, :m]).abs()
-        bound = (2.0 ** -8 + 2 * D[b, :, :m] + 2 * n) * mean_abs[b, :, :m] + 2.0 ** -8 * want[b, :, :m].abs() * 1.01
+        bound = (2.0 ** -8 + 2 * D[b, :, :m] + 2 * n) * mean_abs[b, :, :m] + flush[b, :, :m] + 2.0 ** -8 * want[b, :, :m].abs() * 1.01
         assert torch.all(err <= bound), float((err - bound).max())
         empty = torch.isinf(wlse[b, :, :m])
         assert torch.equal(torch.isinf(lse[b, :, :m]) & (lse[b, :, :m] < 0), empty)
@@ -371,8 +389,8 @@ def test_chunk_by_chunk_generation():
         ds = float((2.0 ** -4 * (qr.double().abs() @ kr.double().abs().transpose(-1, -2)) / math.sqrt(d)).max())
         top = float(v.double().abs().max())
         assert float((o.double() - want).abs().max()) <= (math.exp(min(2 * ds, 20.0)) - 1 + 2.0 ** -4 + 2.0 ** -7) * top
-        ref, _, mean_abs, spread = _reference(cache, qr, nxt)
-        bound = (2.0 ** -8 + 2 * d * 2.0 ** -22 * spread + 2 * 240 * 2.0 ** -23) * mean_abs + 2.0 ** -8 * ref.abs() * 1.01
+        ref, _, mean_abs, flush, spread = _reference(cache, qr, nxt)
+        bound = (2.0 ** -8 + 2 * d * 2.0 ** -22 * spread + 2 * 240 * 2.0 ** -23) * mean_abs + flush + 2.0 ** -8 * ref.abs() * 1.01
         assert torch.all((o.cpu().double() - ref).abs() <= bound)
     assert int(seq[0, 0]) == F * plane
     salad.check_error()
