@@ -18,15 +18,16 @@
 // (rounded by 2^-11); see the softmax for how its maximum and the row sum are
 // kept apart.
 //
-// Warp roles (384 threads, one CTA per SM):
+// Warp roles (512 threads, one CTA per SM):
 //   warps 0..3, 4..7   softmax and output of slots 0 and 1, a row per thread
 //                      (warp w on TMEM lane quarter w % 4); they also load
 //                      their slot's rows of Q
-//   warp 8             TMEM allocation and the single MMA-issuing thread
-//   warps 9..11        codes -> fp16: from a ring of bulk-copied code tiles
-//                      to swizzled operand tiles; warp 9 also issues the bulk
-//                      copies, four operand tiles ahead, and passes the
-//                      blocks' scales to the softmax warps
+//   warps 8..11        codes -> fp16: from a ring of bulk-copied code tiles
+//                      to swizzled operand tiles
+//   warp 12            TMEM allocation and the single MMA-issuing thread
+//   warp 13            bulk copies of code tiles; it also passes the blocks'
+//                      scales to the softmax warps
+//   warps 14, 15       nothing: they fill the warpgroup that gives registers
 // While the tensor pipe runs one slot's PV(t) and QK(t+1), the other slot's
 // softmax runs.  P overwrites S in TMEM.
 //
@@ -45,18 +46,24 @@ namespace {
 
 constexpr int kRows = 256;            // query rows of an item
 constexpr int kTile = 128;            // keys of a tile
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
+// Registers of a thread: at launch, and the warpgroups' shares after it (two
+// of softmax warps, the converting one, the last).  Taking more than the
+// others give would wait forever.
+constexpr int kRegsLaunch = 128, kRegsSoft = 160, kRegsConvert = 112, kRegsLast = 80;
+static_assert(2 * kRegsSoft + kRegsConvert + kRegsLast <= 4 * kRegsLaunch, "register shares");
+static_assert(kThreads * kRegsLaunch == 65536 && kThreads == 4 * 128, "the launch holds the register file");
 
 template <int D>
 struct CT {
   static constexpr int kSlabs = D / 64;
   static constexpr int kRowSlab = 128 * 128;            // 128 rows of 128 bytes
   static constexpr int kOperand = kSlabs * kRowSlab;    // 128 rows of Q, K or V
-  static constexpr int kStages = 3;                     // operand tiles
+  static constexpr int kStages = 4;                     // operand tiles
   static constexpr int kRaw = 128 * D;                  // codes of an operand tile
-  static constexpr int kRaws = 4;
+  static constexpr int kRaws = D == 128 ? 2 : 4;
   static constexpr int kBarBytes = 256;
-  static constexpr int kScaleBytes = 4 * 16 + 4 * 8;    // scales of four tiles (K, K, V, V), four parts' (tiles, slots)
+  static constexpr int kScaleBytes = 8 * 16 + 8 * 8;    // scales of eight tiles (K, K, V, V), eight parts' (tiles, slots)
   static constexpr int kSegBytes = 8 * 64;              // the softmax warps' current parts
   static constexpr int kUsed = (2 + kStages) * kOperand + kRaws * kRaw + kBarBytes + kScaleBytes + kSegBytes;
   // More than half of the SM's shared memory: one CTA (and its 512 TMEM columns) per SM.
@@ -305,6 +312,20 @@ __device__ __forceinline__ void pin64(uint32_t* r) {
   asm volatile("" : SALAD_RW8(r, 48), SALAD_RW8(r, 56));
 }
 
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : SALAD_R8(r, 0), SALAD_R8(r, 8), SALAD_R8(r, 16), SALAD_R8(r, 24)
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void pin32(uint32_t* r) {
+  asm volatile("" : SALAD_RW8(r, 0), SALAD_RW8(r, 8));
+  asm volatile("" : SALAD_RW8(r, 16), SALAD_RW8(r, 24));
+}
+
 // Untiled bulk copy global -> shared completing on `bar`.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile(
@@ -362,32 +383,32 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
   const uint32_t drain = bar(B0 + 10);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + B0 + 11);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  // odd_seg[i % 4] = i + 1: part i's open block holds a value that is not finite.
+  // odd_seg[i % 8] = i + 1: part i's open block holds a value that is not finite.
   volatile int* odd_seg = abort_flag + 1;
-  static_assert((B0 + 11) * 8 + 4 + 4 + 16 <= C::kBarBytes, "barrier region");
-  // Scales of tile i's two blocks in entry i % 4: of the keys (0: no page, its
-  // keys do not count), then of the values.  Warp 9 writes them with the bulk
-  // copy of the tile's keys, at the earliest when the keys of tile i - 2 are
-  // converted: over an operand tile whose MMAs waited for both slots' softmax
-  // of tile i - 4, so that entry has been read.
+  static_assert((B0 + 11) * 8 + 4 + 4 + 32 <= C::kBarBytes, "barrier region");
+  // Scales of tile i's two blocks in entry i % 8: of the keys (0: no page, its
+  // keys do not count), then of the values.  Warp 13 writes them with the bulk
+  // copy of the tile's keys: kRaws operand tiles before these are converted,
+  // and kStages before the MMAs of what they replace, so at most five tiles
+  // before the softmax reads them.
   float4* scales = reinterpret_cast<float4*>(reinterpret_cast<unsigned char*>(bars) + C::kBarBytes);
-  // Tiles and slots of part i in entry i % 4, for the issuer: written and read
+  // Tiles and slots of part i in entry i % 8, for the issuer: written and read
   // like the scales (a part has a tile at least).
-  int2* part_info = reinterpret_cast<int2*>(scales + 4);
+  int2* part_info = reinterpret_cast<int2*>(scales + 8);
   // A softmax warp's current part: registers hold a row of scores instead.
   static_assert(sizeof(Seg) <= 64 && sizeof(Seg) % 4 == 0, "part record");
-  volatile int* seg_mem = reinterpret_cast<volatile int*>(part_info + 4) + 16 * (threadIdx.x / 32 % 8);
+  volatile int* seg_mem = reinterpret_cast<volatile int*>(part_info + 8) + 16 * (threadIdx.x / 32 % 8);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const unsigned long long wait_ns = P.wait_ns;
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(full(i), 3);      // the three converting warps
+      mbar_init(full(i), 4);      // the four converting warps
       mbar_init(empty(i), 1);
     }
     for (int i = 0; i < NR; ++i) {
       mbar_init(raw_full(i), 1);
-      mbar_init(raw_empty(i), 3);
+      mbar_init(raw_empty(i), 4);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full(i), 4);    // the slot's four softmax warps
@@ -398,10 +419,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
-    for (int i = 0; i < 4; ++i) odd_seg[i] = 0;
+    for (int i = 0; i < 8; ++i) odd_seg[i] = 0;
     fence_mbar_init();
   }
-  if (warp == 8) {
+  if (warp == 12) {
     tmem_alloc(smem_u32(tmem_holder), C::kCols);
     tmem_relinquish();
   }
@@ -410,11 +431,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
 
-  // Register shares, 3 x 168 in all: 192 for each softmax warpgroup, 120 for
-  // the other.
-  if (warp == 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
-    if (lane == 0) {
+  // Every warp of every warpgroup passes one of these three.
+  if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLast));
+    if (warp == 12 && lane == 0) {
       // ===================================================== MMA issuer
       constexpr uint32_t idesc_qk = idesc_f16(128, 128, false, false);
       constexpr uint32_t idesc_pv = idesc_f16(128, D, false, true);
@@ -426,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
       uint32_t ph = 0;
       uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};
       bool ok = true;
-      auto wait_stage = [&]() -> bool { return mbar_wait(full(st), ph, wait_ns, abort_flag); };
+      auto wait_stage = [&]() -> bool { return mbar_wait_poll(full(st), ph, wait_ns, abort_flag); };
       auto next_stage = [&]() {
         mma_commit(empty(st));
         if (++st == NS) {
@@ -446,10 +466,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
       int left = static_cast<int>(w1 - w0);
       for (int part_no = 0; left > 0 && ok; ++part_no) {
         if (!wait_stage()) { ok = false; break; }
-        const int2 info = part_info[part_no % 4];
+        const int2 info = part_info[part_no % 8];
         const int n = info.x, slots = info.y;
         for (int slot = 0; slot < slots && ok; ++slot) {
-          ok = mbar_wait(q_full(slot), qn[slot]++ & 1u, wait_ns, abort_flag);
+          ok = mbar_wait_poll(q_full(slot), qn[slot]++ & 1u, wait_ns, abort_flag);
           if (!ok) break;
           tc_fence_after();
           issue_qk(slot, st);
@@ -463,17 +483,18 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
           const int kst = st + 1 == NS ? 0 : st + 1;
           const uint32_t kph = st + 1 == NS ? ph ^ 1u : ph;
           for (int slot = 0; slot < slots && ok; ++slot) {
-            ok = mbar_wait(p_full(slot), pn[slot]++ & 1u, wait_ns, abort_flag) && (slot > 0 || wait_stage());
+            ok = mbar_wait_spin(p_full(slot), pn[slot]++ & 1u, wait_ns, abort_flag) && (slot > 0 || wait_stage());
             if (!ok) break;
             tc_fence_after();
             const uint32_t sa = tmem + C::s_col(slot), oa = tmem + C::o_col(slot);
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)      // 16 keys each
-              mma_ts(oa, sa + ks * 8, vd + static_cast<uint64_t>((ks * 2048) >> 4), idesc_pv,
+              mma_ts(oa, sa + 64 + ks * 8, vd + static_cast<uint64_t>((ks * 2048) >> 4), idesc_pv,
                      ks > 0 ? 1u : (t > 0 ? 1u : 0u));
-            mma_commit(o_done(slot));
-            if (t + 1 < n) {
-              if (slot == 0 && !mbar_wait(full(kst), kph, wait_ns, abort_flag)) { ok = false; break; }
+            if (t + 1 == n) {
+              mma_commit(o_done(slot));
+            } else {
+              if (slot == 0 && !mbar_wait_poll(full(kst), kph, wait_ns, abort_flag)) { ok = false; break; }
               tc_fence_after();
               issue_qk(slot, kst);               // over this slot's P: behind its PV in issue order
               if (t + 2 == n) mma_commit(q_free(slot));
@@ -487,115 +508,115 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
       }
       if (!ok) raise_timeout(P.err, abort_flag);
       mma_commit(drain);
-      if (!mbar_wait(drain, 0, wait_ns, nullptr)) atomicOr(P.err, kErrTimeout);
+      if (!mbar_wait_poll(drain, 0, wait_ns, nullptr)) atomicOr(P.err, kErrTimeout);
+    } else if (warp == 13) {
+      // ===================================================== bulk copies
+      struct Blocks {                             // of 32 blocks, one per lane
+        int page;                                 // -2: not closed
+        float ks, vs;
+      };
+      // A table entry that is no page reads page 0; a key scale of 0 masks it.
+      auto blocks_at = [&](const Seg& g, int blk) {
+        Blocks k{-2, 1.0f, 1.0f};
+        if (blk + lane < g.s.len / kCacheBlock) {
+          k.page = cache_page(__ldg(P.c.page_table + static_cast<long long>(g.b) * P.c.blocks + blk + lane), P.c.pages);
+          if (k.page < 0) {
+            k.page = 0;
+            k.ks = 0.0f;
+            atomicOr(P.err, kErrRange);
+          } else {
+            const long long at = static_cast<long long>(k.page) * P.c.H + g.h;
+            k.ks = __ldg(P.c.k_scale + at);
+            k.vs = __ldg(P.c.v_scale + at);
+          }
+        }
+        return k;
+      };
+      // Scale of the open block's finite keys or values.
+      auto open_scale = [&](const Seg& g, const void* base) {
+        const uint4* tail = reinterpret_cast<const uint4*>(
+            static_cast<const __nv_bfloat16*>(base) +
+            ((static_cast<long long>(g.b) * 2 + g.s.slot) * P.c.H + g.h) * kCacheBlock * D);
+        const int n = g.s.len % kCacheBlock * (D / 8);
+        uint32_t top = 0;
+#pragma unroll 8
+        for (int e = lane; e < n; e += 32) {
+          const uint4 x = __ldg(tail + e);
+          top = __vmaxu2(top, finite_or_zero(x.x) & 0x7fff7fffu);
+          top = __vmaxu2(top, finite_or_zero(x.y) & 0x7fff7fffu);
+          top = __vmaxu2(top, finite_or_zero(x.z) & 0x7fff7fffu);
+          top = __vmaxu2(top, finite_or_zero(x.w) & 0x7fff7fffu);
+        }
+        return tail_scale(__reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16)));
+      };
+      uint32_t at = 0, tile_no = 0;               // operand tiles and key tiles so far
+      int part_no = 0;
+      bool ok = true;
+      for (Seg g = seg_at(T, w0, w1 - w0); g.left > 0 && ok; g = seg_next(P, g), ++part_no) {
+        // 16 tiles' blocks, and the 16 after them (loaded 16 tiles early).
+        Blocks cur{}, nxt = blocks_at(g, 2 * (g.all.first + g.t0));
+#pragma unroll 1
+        for (int t = g.t0; t < g.t1 && ok; ++t, ++tile_no) {
+          const int j = g.all.first + t, i = (t - g.t0) % 16;
+          if (i == 0) {
+            cur = nxt;
+            nxt = blocks_at(g, 2 * j + 32);
+          }
+          float4 sc = make_float4(__shfl_sync(0xffffffffu, cur.ks, 2 * i), __shfl_sync(0xffffffffu, cur.ks, 2 * i + 1),
+                                  __shfl_sync(0xffffffffu, cur.vs, 2 * i), __shfl_sync(0xffffffffu, cur.vs, 2 * i + 1));
+          const int p0 = __shfl_sync(0xffffffffu, cur.page, 2 * i), p1 = __shfl_sync(0xffffffffu, cur.page, 2 * i + 1);
+          const int open = g.s.len / kCacheBlock - 2 * j;
+          if (open == 0 || open == 1) {
+            const float ks = open_scale(g, P.c.k_tail), vs = open_scale(g, P.c.v_tail);
+            (open ? sc.y : sc.x) = ks;
+            (open ? sc.w : sc.z) = vs;
+          }
+#pragma unroll 1
+          for (int value = 0; value < 2 && ok; ++value, ++at) {
+            const int rs = static_cast<int>(at % NR);
+            const uint32_t n = at / NR;
+            ok = n == 0 || __all_sync(0xffffffffu, mbar_wait_poll(raw_empty(rs), (n - 1) & 1u, wait_ns, abort_flag));
+            if (!ok) break;
+            if (lane == 0) {
+              if (!value) {
+                if (t == g.t0) part_info[part_no % 8] = make_int2(g.t1 - g.t0, g.two ? 2 : 1);
+                scales[tile_no % 8] = sc;
+              }
+              constexpr uint32_t bytes = kCacheBlock * D;
+              const unsigned char* pages = value ? P.c.v_pages : P.c.k_pages;
+              const uint32_t dst = smem_u32(raws) + rs * C::kRaw;
+              mbar_arrive_expect_tx(raw_full(rs), (p0 >= 0 ? bytes : 0u) + (p1 >= 0 ? bytes : 0u));
+              if (p0 >= 0) bulk_load(dst, pages + (static_cast<long long>(p0) * P.c.H + g.h) * bytes, bytes, raw_full(rs));
+              if (p1 >= 0) bulk_load(dst + bytes, pages + (static_cast<long long>(p1) * P.c.H + g.h) * bytes, bytes, raw_full(rs));
+            }
+            __syncwarp();
+          }
+        }
+      }
+      if (!ok) raise_timeout(P.err, abort_flag);
+      // No bulk copy may be in flight at the exit.
+      if (lane == 0) {
+        for (uint32_t i = 0; i < NR && i < at; ++i) {
+          const uint32_t last = (at - 1 - i) / NR;            // turns of raw slot i, less one
+          if (!mbar_wait_poll(raw_full(static_cast<int>(i)), last & 1u, wait_ns, nullptr)) atomicOr(P.err, kErrTimeout);
+        }
+      }
     }
-  } else if (warp > 8) {
+  } else if (warp >= 8) {
     // ================================================== codes -> fp16
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
-    const int w = warp - 9;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
+    const int w = warp - 8;
     constexpr int CPR = D / 16;                 // 16-code chunks of a row
     constexpr int RU = 32 / CPR;                // rows of one warp step
-    const int c = lane % CPR, rl = lane / CPR;
+    constexpr int kSteps = 128 / (4 * RU);
+    const int c = lane % CPR, row0 = w * RU + lane / CPR;
     // Which eight codes of a lane's sixteen go first: chosen so that neither
     // the 8-byte reads nor the swizzled 16-byte writes meet in a bank.
-    const int swap = D == 128 ? (c >> 2) ^ (rl & 1) : (rl >> 1) & 1;
+    const int swap = D == 128 ? (c >> 2) ^ (row0 & 1) : (row0 >> 1) & 1;
+    const int from0 = row0 * D + 16 * c + 8 * swap, from1 = row0 * D + 16 * c + 8 * (swap ^ 1);
+    const int to = (c / 4) * C::kRowSlab + row0 * 128, ch = (2 * c) & 7;
+    const int to0 = to + (((ch + swap) ^ (row0 & 7)) << 4), to1 = to + (((ch + (swap ^ 1)) ^ (row0 & 7)) << 4);
     bool ok = true;
-
-    // ---- warp 9: bulk copies, ahead of the conversion.
-    struct Blocks {                             // of 32 blocks, one per lane
-      int page;                                 // -2: not closed
-      float ks, vs;
-    };
-    // A table entry that is no page reads page 0; a key scale of 0 masks it.
-    auto blocks_at = [&](const Seg& g, int blk) {
-      Blocks k{-2, 1.0f, 1.0f};
-      if (blk + lane < g.s.len / kCacheBlock) {
-        k.page = cache_page(__ldg(P.c.page_table + static_cast<long long>(g.b) * P.c.blocks + blk + lane), P.c.pages);
-        if (k.page < 0) {
-          k.page = 0;
-          k.ks = 0.0f;
-          atomicOr(P.err, kErrRange);
-        } else {
-          const long long at = static_cast<long long>(k.page) * P.c.H + g.h;
-          k.ks = __ldg(P.c.k_scale + at);
-          k.vs = __ldg(P.c.v_scale + at);
-        }
-      }
-      return k;
-    };
-    // Scale of the open block's finite keys or values.
-    auto open_scale = [&](const Seg& g, const void* base) {
-      const uint4* tail = reinterpret_cast<const uint4*>(
-          static_cast<const __nv_bfloat16*>(base) +
-          ((static_cast<long long>(g.b) * 2 + g.s.slot) * P.c.H + g.h) * kCacheBlock * D);
-      const int n = g.s.len % kCacheBlock * (D / 8);
-      uint32_t top = 0;
-#pragma unroll 8
-      for (int e = lane; e < n; e += 32) {
-        const uint4 x = __ldg(tail + e);
-        top = __vmaxu2(top, finite_or_zero(x.x) & 0x7fff7fffu);
-        top = __vmaxu2(top, finite_or_zero(x.y) & 0x7fff7fffu);
-        top = __vmaxu2(top, finite_or_zero(x.z) & 0x7fff7fffu);
-        top = __vmaxu2(top, finite_or_zero(x.w) & 0x7fff7fffu);
-      }
-      return tail_scale(__reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16)));
-    };
-    Seg pg = seg_at(T, w0, w1 - w0);            // next operand tile to copy
-    int pt = pg.t0, p_part = 0;
-    bool p_value = false;
-    uint32_t p_at = 0, p_tile = 0;
-    Blocks cur{}, nxt{};
-    auto produce = [&]() -> bool {
-      if (pg.left <= 0) return true;
-      const int rs = static_cast<int>(p_at % NR);
-      const uint32_t n = p_at / NR;
-      if (n > 0 && !__all_sync(0xffffffffu, mbar_wait(raw_empty(rs), (n - 1) & 1u, wait_ns, abort_flag))) return false;
-      const int j = pg.all.first + pt, i = (pt - pg.t0) % 16;
-      if (!p_value) {
-        if (pt == pg.t0) nxt = blocks_at(pg, 2 * j);
-        if (i == 0) {
-          cur = nxt;
-          nxt = blocks_at(pg, 2 * j + 32);      // needed 16 tiles on
-        }
-        float4 sc = make_float4(__shfl_sync(0xffffffffu, cur.ks, 2 * i), __shfl_sync(0xffffffffu, cur.ks, 2 * i + 1),
-                                __shfl_sync(0xffffffffu, cur.vs, 2 * i), __shfl_sync(0xffffffffu, cur.vs, 2 * i + 1));
-        const int open = pg.s.len / kCacheBlock - 2 * j;
-        if (open == 0 || open == 1) {
-          const float ks = open_scale(pg, P.c.k_tail), vs = open_scale(pg, P.c.v_tail);
-          (open ? sc.y : sc.x) = ks;
-          (open ? sc.w : sc.z) = vs;
-        }
-        if (lane == 0) {
-          if (pt == pg.t0) part_info[p_part % 4] = make_int2(pg.t1 - pg.t0, pg.two ? 2 : 1);
-          scales[p_tile % 4] = sc;
-        }
-      }
-      const int p0 = __shfl_sync(0xffffffffu, cur.page, 2 * i), p1 = __shfl_sync(0xffffffffu, cur.page, 2 * i + 1);
-      if (lane == 0) {
-        constexpr uint32_t bytes = kCacheBlock * D;
-        const unsigned char* pages = p_value ? P.c.v_pages : P.c.k_pages;
-        const uint32_t dst = smem_u32(raws) + rs * C::kRaw;
-        mbar_arrive_expect_tx(raw_full(rs), (p0 >= 0 ? bytes : 0u) + (p1 >= 0 ? bytes : 0u));
-        if (p0 >= 0) bulk_load(dst, pages + (static_cast<long long>(p0) * P.c.H + pg.h) * bytes, bytes, raw_full(rs));
-        if (p1 >= 0) bulk_load(dst + bytes, pages + (static_cast<long long>(p1) * P.c.H + pg.h) * bytes, bytes, raw_full(rs));
-      }
-      __syncwarp();
-      ++p_at;
-      if (p_value) {
-        ++p_tile;
-        if (++pt == pg.t1) {
-          pg = seg_next(P, pg);
-          pt = pg.t0;
-          ++p_part;
-        }
-      }
-      p_value = !p_value;
-      return true;
-    };
-    if (w == 0)
-      for (int i = 0; i < NR && ok; ++i) ok = produce();
-
-    // ---- conversion, operand tile by operand tile
     Seg g = seg_at(T, w0, w1 - w0);
     int part_no = 0;
     uint32_t tile_no = 0;
@@ -607,28 +628,28 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
         const bool value = o & 1;
         const int j = g.all.first + (o >> 1);
         const int closed = g.s.len / kCacheBlock - 2 * j;   // of the tile's blocks: 2 and more, 1, 0 and less
-        if (!__all_sync(0xffffffffu, mbar_wait(raw_full(rs), rph, wait_ns, abort_flag) &&
-                                         mbar_wait(empty(st), sph, wait_ns, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait_poll(raw_full(rs), rph, wait_ns, abort_flag) &&
+                                         mbar_wait_poll(empty(st), sph, wait_ns, abort_flag))) {
           ok = false;
           break;
         }
         const unsigned char* src = raws + rs * C::kRaw;
         unsigned char* dst = ring + st * C::kOperand;
-        const float4 sc = scales[tile_no % 4];
+        const float4 sc = scales[tile_no % 8];
         // Value blocks of NaN, or of no page, are left out here (their codes
         // may be NaN; the softmax marks the rows that see them).
         const bool out0 = value && (isnan(sc.z) || sc.x == 0.0f), out1 = value && (isnan(sc.w) || sc.y == 0.0f);
         const int first = closed >= 1 && !out0 ? 0 : 64, last = closed >= 2 && !out1 ? 128 : 64;
-#pragma unroll 4
-        for (int r0 = first + w * RU; r0 < last; r0 += 3 * RU) {
-          const int row = r0 + rl;
-          const unsigned char* from = src + row * D + 16 * c;
-          const uint2 a = *reinterpret_cast<const uint2*>(from + 8 * swap);
-          const uint2 b = *reinterpret_cast<const uint2*>(from + 8 * (swap ^ 1));
-          unsigned char* to = dst + (c / 4) * C::kRowSlab + row * 128;
-          const int ch = (2 * c) & 7;
-          *reinterpret_cast<uint4*>(to + (((ch + swap) ^ (row & 7)) << 4)) = eight_codes(a);
-          *reinterpret_cast<uint4*>(to + (((ch + (swap ^ 1)) ^ (row & 7)) << 4)) = eight_codes(b);
+        // Four warps: warp w's rows are row0 + (128 / kSteps) i, whose place in
+        // the swizzle is the same for every i.
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          const int row = row0 + (128 / kSteps) * i;
+          if (row < first || row >= last) continue;
+          const uint2 a = *reinterpret_cast<const uint2*>(src + from0 + (128 / kSteps) * D * i);
+          const uint2 b = *reinterpret_cast<const uint2*>(src + from1 + (128 / kSteps) * D * i);
+          *reinterpret_cast<uint4*>(dst + to0 + (128 / kSteps) * 128 * i) = eight_codes(a);
+          *reinterpret_cast<uint4*>(dst + to1 + (128 / kSteps) * 128 * i) = eight_codes(b);
         }
         if (last - first < 128) {
           // The open block's rows, scaled, and zeros elsewhere.  Values that
@@ -642,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
           const int held = g.s.len % kCacheBlock;
           bool odd = false;
 #pragma unroll 1
-          for (int e = w * 32 + lane; e < 128 * (D / 8); e += 96) {
+          for (int e = w * 32 + lane; e < 128 * (D / 8); e += 128) {
             const int row = e / (D / 8), ch = e % (D / 8);
             if (row >= first && row < last) continue;
             uint4 x = make_uint4(0u, 0u, 0u, 0u);
@@ -657,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
             }
             *reinterpret_cast<uint4*>(dst + (ch / 8) * C::kRowSlab + row * 128 + (((ch % 8) ^ (row & 7)) << 4)) = x;
           }
-          if (odd) odd_seg[part_no % 4] = part_no + 1;
+          if (odd) odd_seg[part_no % 8] = part_no + 1;
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -674,27 +695,19 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
           rph ^= 1u;
         }
         if (value) ++tile_no;
-        if (w == 0) ok = produce();
       }
       ++part_no;
       g = seg_next(P, g);
     }
     if (!ok) raise_timeout(P.err, abort_flag);
-    // No bulk copy may be in flight at the exit.
-    if (w == 0 && lane == 0) {
-      for (uint32_t i = 0; i < NR && i < p_at; ++i) {
-        const uint32_t last = (p_at - 1 - i) / NR;          // turns of raw slot i, less one
-        if (!mbar_wait(raw_full(static_cast<int>(i)), last & 1u, wait_ns, nullptr)) atomicOr(P.err, kErrTimeout);
-      }
-    }
   } else {
     // ============================================ softmax and output
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     const int slot = warp / 4, quarter = warp % 4;
     const int r = quarter * 32 + lane;                  // row of the slot (TMEM lane)
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t sbuf = lane_base + C::s_col(slot), obuf = lane_base + C::o_col(slot);
-    uint32_t sn = 0, on = 0, parts = 0;                 // S tiles, PVs and parts of this slot so far
+    uint32_t sn = 0, parts = 0;                         // S tiles and parts of this slot so far
     bool ok = true;
     // This slot's rows of a part's Q into shared memory (zeros where there is
     // no row), scaled; returns what the row's scores are to be multiplied by.
@@ -781,13 +794,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
         float ev_top = -INFINITY;                       // largest ev so far
         bool vbad = false;
         for (int t = 0; t < n; ++t) {
-          if (!__all_sync(0xffffffffu, mbar_wait(s_full(slot), sn & 1u, wait_ns, abort_flag))) {
+          if (!__all_sync(0xffffffffu, mbar_wait_poll(s_full(slot), sn & 1u, wait_ns, abort_flag))) {
             ok = false;
             break;
           }
           ++sn;
           tc_fence_after();
-          const float4 sc = scales[(tile_no + t) % 4];
+          const float4 sc = scales[(tile_no + t) % 8];
           const int kb = (j0 + t) * kTile;
           // Halves outside some row's range: scores there become -inf, in
           // TMEM.  (A NaN key scale makes the scores that are seen NaN; a NaN
@@ -812,11 +825,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
             }
             tmem_st_wait();
           }
-          // The tile's scores of this row, in registers.
-          uint32_t sv[128];
+          // Pass 1: the row's maxima.  The second half's scores stay in
+          // registers; the first half's are read again in pass 2.
+          uint32_t sv[64], sw[64];
           tmem_ld64_async(sbuf, sv);
           tmem_arrived();
-          tmem_ld64_async(sbuf + 64, sv + 64);          // travels while the first half is reduced
+          tmem_ld64_async(sbuf + 64, sw);               // travels while the first half is reduced
           pin64(sv);
           const float c20 = isnan(sc.x) ? 1.0f : fmaxf(c1 * sc.x, 1e-37f);   // positive: -inf stays -inf
           const float c21 = isnan(sc.y) ? 1.0f : fmaxf(c1 * sc.y, 1e-37f);
@@ -824,8 +838,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
           ev_top = fmaxf(ev_top, fmaxf(ev0, ev1));
           const float s0 = max64(sv) * c20;
           tmem_arrived();
-          pin64(sv + 64);
-          const float s1 = max64(sv + 64) * c21;
+          pin64(sw);
+          const float s1 = max64(sw) * c21;
           const float pm = fmaxf(s0 + ev0, s1 + ev1);
           float f = 1.0f;
           if (pm > mt + 8.0f) {
@@ -840,64 +854,76 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
           // A row that has seen no key: exp2(-inf - 0) = 0.
           const float nm = mt == -INFINITY ? 0.0f : -mt, ns = ms == -INFINITY ? 0.0f : -ms;
           float add = 0.0f;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float c2 = x ? c21 : c20, ev = x ? ev1 : ev0;
-            const uint64_t c22 = pack2(c2, c2), off = pack2(nm + ev, nm + ev);
-            uint64_t a0 = 0, a1 = 0;
-            if (ev_top - ev > 90.0f) {
-              // P may vanish beside another block's; the sum must not.
+          // Sum of the weights of half x where P may vanish beside another
+          // block's but the sum must not.
+          auto far_sum = [&](int x, float c2) {
 #pragma unroll 1
-              for (int c0 = 0; c0 < 64; c0 += 32) {
-                uint32_t s32[32];
-                tmem_ld32(sbuf + 64 * x + c0, s32);
-#pragma unroll
-                for (int c = 0; c < 32; ++c) add += ex2_ftz(fmaf(__uint_as_float(s32[c]), c2, ns));
-              }
-            }
-#pragma unroll
             for (int c0 = 0; c0 < 64; c0 += 32) {
-              uint32_t pk[16];
+              uint32_t s32[32];
+              tmem_ld32(sbuf + 64 * x + c0, s32);
 #pragma unroll
-              for (int c = 0; c < 32; c += 4) {
-                const uint32_t* v = sv + 64 * x + c0 + c;
-                float p0, p1, p2, p3;
-                unpack2(fma2(pack2(__uint_as_float(v[0]), __uint_as_float(v[1])), c22, off), p0, p1);
-                unpack2(fma2(pack2(__uint_as_float(v[2]), __uint_as_float(v[3])), c22, off), p2, p3);
-                p0 = ex2_ftz(p0);
-                p1 = ex2_ftz(p1);
-                p2 = ex2_ftz(p2);
-                p3 = ex2_ftz(p3);
-                pk[c / 2] = pack_f16x2(p0, p1);
-                pk[c / 2 + 1] = pack_f16x2(p2, p3);
-                a0 = add2(a0, pack2(p0, p1));
-                a1 = add2(a1, pack2(p2, p3));
-              }
-              tmem_st16(sbuf + 32 * x + c0 / 2, pk);
+              for (int c = 0; c < 32; ++c) add += ex2_ftz(fmaf(__uint_as_float(s32[c]), c2, ns));
             }
+          };
+          const bool far0 = ev_top - ev0 > 90.0f, far1 = ev_top - ev1 > 90.0f;
+          if (far1) far_sum(1, c21);
+          if (far0) far_sum(0, c20);
+          // Pass 2: 32 scores as 16 pairs of P, at columns 64 and up of S (the
+          // second half's scores have left them).
+          uint64_t sum0 = 0, sum1 = 0;
+          auto weights = [&](const uint32_t* v, uint64_t c22, uint64_t off, uint32_t to) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {
+              float p0, p1, p2, p3;
+              unpack2(fma2(pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), c22, off), p0, p1);
+              unpack2(fma2(pack2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])), c22, off), p2, p3);
+              p0 = ex2_ftz(p0);
+              p1 = ex2_ftz(p1);
+              p2 = ex2_ftz(p2);
+              p3 = ex2_ftz(p3);
+              pk[c / 2] = pack_f16x2(p0, p1);
+              pk[c / 2 + 1] = pack_f16x2(p2, p3);
+              sum0 = add2(sum0, pack2(p0, p1));
+              sum1 = add2(sum1, pack2(p2, p3));
+            }
+            tmem_st16(to, pk);
+          };
+          auto take_sum = [&](bool far, float ev) {
             float u0, u1;
-            unpack2(add2(a0, a1), u0, u1);
-            if (!(ev_top - ev > 90.0f)) add = fmaf(u0 + u1, ex2_ftz(ns - nm - ev), add);
+            unpack2(add2(sum0, sum1), u0, u1);
+            if (!far) add = fmaf(u0 + u1, ex2_ftz(ns - nm - ev), add);
+            sum0 = sum1 = 0;
+          };
+          {
+            const uint64_t c22 = pack2(c21, c21), off = pack2(nm + ev1, nm + ev1);
+            tmem_ld32_async(sbuf, sv);
+            weights(sw, c22, off, sbuf + 96);
+            weights(sw + 32, c22, off, sbuf + 112);
+            take_sum(far1, ev1);
+          }
+          {
+            const uint64_t c22 = pack2(c20, c20), off = pack2(nm + ev0, nm + ev0);
+            tmem_arrived();
+            pin32(sv);
+            tmem_ld32_async(sbuf + 32, sv + 32);
+            weights(sv, c22, off, sbuf + 64);
+            tmem_arrived();
+            pin32(sv + 32);
+            weights(sv + 32, c22, off, sbuf + 80);
+            take_sum(far0, ev0);
           }
           l += add;
-          // Every PV of the slot is observed in order: a parity wait is at
-          // most one phase behind.
-          if (t > 0) {
-            if (!__all_sync(0xffffffffu, mbar_wait(o_done(slot), on & 1u, wait_ns, abort_flag))) {
-              ok = false;
-              break;
-            }
-            ++on;
-            tc_fence_after();
-            if (__any_sync(0xffffffffu, f != 1.0f)) {
+          // The slot's previous PV was issued before this tile's QK, whose
+          // commit has arrived: O may be rescaled.
+          if (t > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
 #pragma unroll 1
-              for (int c0 = 0; c0 < D; c0 += 32) {
-                uint32_t o32[32];
-                tmem_ld32(obuf + c0, o32);
+            for (int c0 = 0; c0 < D; c0 += 32) {
+              uint32_t o32[32];
+              tmem_ld32(obuf + c0, o32);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o32[e] = __float_as_uint(__uint_as_float(o32[e]) * f);
-                tmem_st32(obuf + c0, o32);
-              }
+              for (int e = 0; e < 32; ++e) o32[e] = __float_as_uint(__uint_as_float(o32[e]) * f);
+              tmem_st32(obuf + c0, o32);
             }
           }
           tmem_st_wait();
@@ -907,7 +933,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
         }
         if (!ok) break;
         // Every QK of the part has run: the next part's Q, while its last PV does.
-        if (!__all_sync(0xffffffffu, mbar_wait(q_free(slot), parts & 1u, wait_ns, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait_poll(q_free(slot), parts & 1u, wait_ns, abort_flag))) {
           ok = false;
           break;
         }
@@ -917,15 +943,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
         const Seg ng = seg_next(P, g);
         keep_seg(ng);
         start(ng);
-        if (!__all_sync(0xffffffffu, mbar_wait(o_done(slot), on & 1u, wait_ns, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait_poll(o_done(slot), (parts - 1) & 1u, wait_ns, abort_flag))) {
           ok = false;
           break;
         }
-        ++on;
         tc_fence_after();
         // ---- output: O is in units of 2^mt, the sum of 2^ms
         const bool whole = g.t0 == 0 && g.t1 == g.all.n;
-        const bool odd = odd_seg[part_no % 4] == part_no + 1;
+        const bool odd = odd_seg[part_no % 8] == part_no + 1;
         const float unit = mt == -INFINITY ? 1.0f : ex2_ftz(mt - ms);
         const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
         char* orow = P.o + g.b * P.ob + row.head * P.oh + row.n * P.on;
@@ -980,7 +1005,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == 12) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kCols);
   }
