@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from typing import Optional, Sequence
 
 import torch
@@ -130,6 +131,14 @@ class CacheAttnArgs(ctypes.Structure):
     ]
 
 
+# The last three structs in struct module notation: filling a ctypes mirror
+# field by field costs a single-token call more than its kernel.
+_CACHE = "7P5i"
+_PACK_ROPE = struct.Struct("@4P12q6iP4i3ifii")
+_PACK_APPEND = struct.Struct(f"@{_CACHE}4P6qiPiP6ifi")
+_PACK_ATTN = struct.Struct(f"@{_CACHE}3P6qP2iP2ifPN")
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libsalad.so not built ({LIB_PATH}); run "
@@ -157,10 +166,11 @@ def _load() -> ctypes.CDLL:
         "salad_check_error": (i, [vp]),
         "salad_debug_wait_timeout": (i, [ctypes.c_ulonglong, vp]),
         "salad_gate_noalloc": (i, [vp, vp, f, i, i, i, vp, vp]),
-        "salad_rope": (i, [ctypes.POINTER(RopeArgs), vp]),
-        "salad_cache_append": (i, [ctypes.POINTER(CacheAppendArgs), vp]),
-        "salad_cache_attn_workspace_bytes": (sz, [ctypes.POINTER(CacheAttnArgs)]),
-        "salad_cache_attn": (i, [ctypes.POINTER(CacheAttnArgs), vp]),
+        # Argument structs as packed bytes (or a pointer to one of the mirrors).
+        "salad_rope": (i, [vp, vp]),
+        "salad_cache_append": (i, [vp, vp]),
+        "salad_cache_attn_workspace_bytes": (sz, [vp]),
+        "salad_cache_attn": (i, [vp, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -179,7 +189,9 @@ class _Lib:
     def __getattr__(self, name):
         if _Lib._cdll is None:
             _Lib._cdll = _load()
-        return getattr(_Lib._cdll, name)
+        fn = getattr(_Lib._cdll, name)
+        self.__dict__[name] = fn       # later lookups do not come here
+        return fn
 
 
 lib = _Lib()
@@ -251,20 +263,44 @@ def _workspace(nbytes: int, device, workspace: Optional[torch.Tensor]) -> Option
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
-def _dev_rows(t, dtype, name: str) -> Strides:
-    """A [B, H, N, d] tensor with contiguous rows of d and any other strides,
-    on the current device; returns its strides."""
+def _device_of(t, name: str) -> int:
+    """The current device's index, which must be t's."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    if t.dtype != dtype:
+    dev = torch.cuda.current_device()
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
+    return dev
+
+
+def _rows(t, shape, dtype, dev: int, name: str):
+    """A [B, H, N, d] tensor of a shape and dtype with contiguous rows and any
+    other strides, on the current device; returns (batch, head, token) strides."""
+    if not isinstance(t, torch.Tensor) or t.shape != shape:
+        _shape(t, shape, name)
+    if t.get_device() != dev or t.dtype != dtype:
+        _device_of(t, name)
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     b, h, n, c = t.stride()
     if c != 1:
         raise ValueError(f"{name} must have contiguous rows (the last dimension's stride is {c})")
-    return Strides(b, h, n)
+    return b, h, n
+
+
+def _flat(t, shape, dtype, dev: int, name: str) -> int:
+    """Address of a contiguous tensor of a shape and dtype on the current device."""
+    if not isinstance(t, torch.Tensor) or t.shape != shape:
+        _shape(t, shape, name)
+    if t.get_device() != dev or t.dtype != dtype or not t.is_contiguous():
+        _dev_tensor(t, dtype, name)
+    return t.data_ptr()
+
+
+def _stream_on(stream, dev: int) -> int:
+    """The call's stream: the current one of the device, or the one given."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
 
 
 def _flags(space_major_heads, H: int):
@@ -423,61 +459,67 @@ def _empty_on(stream, make):
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _PAIRINGS = {"adjacent": 0, "halves": 1}
-_NO_STRIDES = Strides(0, 0, 0)
+_NO_STRIDES = (0, 0, 0)
 
 
-def _rotation(d: int, split, pairing: str, positions, grid, B: int, N: int):
-    """(split, pairing, batched, Hh, Wh) of a rotation, checked."""
+def _rotation(d: int, split, pairing: str, positions, grid, B: int, N: int, dev: int):
+    """(split, pairing, positions, batched, Hh, Wh) of a rotation, checked."""
     if split is None:
         dy = 2 * (d // 6)
         split = (d - 2 * dy, dy, dy)
-    if len(split) != 3:
+    elif len(split) != 3:
         raise ValueError("split must name the channels of three axes")
-    if pairing not in _PAIRINGS:
+    pair = _PAIRINGS.get(pairing)
+    if pair is None:
         raise ValueError(f"pairing must be one of {sorted(_PAIRINGS)}")
     if (positions is None) == (grid is None):
         raise ValueError("give the tokens' positions or their grid")
-    batched, Hh, Wh = 0, 0, 0
-    if positions is not None:
-        _dev_tensor(positions, torch.int32, "positions")
-        batched = int(positions.dim() == 3)
-        _shape(positions, (B, N, 3) if batched else (N, 3), "positions")
-    else:
-        Hh, Wh = grid
-    return tuple(int(c) for c in split), _PAIRINGS[pairing], batched, int(Hh), int(Wh)
+    if positions is None:
+        return split, pair, 0, 0, grid[0], grid[1]
+    batched = int(isinstance(positions, torch.Tensor) and positions.dim() == 3)
+    return (split, pair, _flat(positions, (B, N, 3) if batched else (N, 3), torch.int32, dev, "positions"), batched,
+            0, 0)
+
+
+def _pack(fmt: struct.Struct, what: str, *values) -> bytes:
+    try:
+        return fmt.pack(*values)
+    except struct.error as e:      # a number that its C type does not hold
+        raise ValueError(f"{what}: {e}") from None
 
 
 def _rope(what: str, q, k, positions, grid, offset, base, split, pairing, inverse, q_out, k_out,
           stream):
     _dims(q, 4, "q", "[B, H, N, d]")
-    B, Hq, N, d = q.shape
-    if q.dtype not in _DTYPES:
-        raise ValueError(f"q must be bfloat16, float16 or float32, got {q.dtype}")
+    dtype, dev = q.dtype, _device_of(q, "q")
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise ValueError(f"q must be bfloat16, float16 or float32, got {dtype}")
     if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
         raise ValueError(f"{what} is not recorded by autograd: call it under torch.no_grad() and "
                          "turn the gradients with rope_backward")
-    if q_out is not None:
-        _shape(q_out, q.shape, "q_out")
-    q_st = _dev_rows(q, q.dtype, "q")
-    q_out = _empty_on(stream, lambda: torch.empty_like(q)) if q_out is None else q_out
-    qo_st = _dev_rows(q_out, q.dtype, "q_out")
-    Hk, k_st, ko_st = 0, _NO_STRIDES, _NO_STRIDES
+    shape = q.shape
+    B, Hq, N, d = shape
+    q_st = _rows(q, shape, dtype, dev, "q")
+    if q_out is None:
+        q_out = _empty_on(stream, lambda: torch.empty_like(q))
+    qo_st = _rows(q_out, shape, dtype, dev, "q_out")
     if k is not None:
         _dims(k, 4, "k", "[B, H, N, d]")
         Hk = k.shape[1]
-        _shape(k, (B, Hk, N, d), "k")
-        if k_out is not None:
-            _shape(k_out, k.shape, "k_out")
-        k_st = _dev_rows(k, q.dtype, "k")
-        k_out = _empty_on(stream, lambda: torch.empty_like(k)) if k_out is None else k_out
-        ko_st = _dev_rows(k_out, q.dtype, "k_out")
+        k_st = _rows(k, (B, Hk, N, d), dtype, dev, "k")
+        if k_out is None:
+            k_out = _empty_on(stream, lambda: torch.empty_like(k))
+        ko_st = _rows(k_out, k.shape, dtype, dev, "k_out")
+        kp, kop = k.data_ptr(), k_out.data_ptr()
     elif k_out is not None:
         raise ValueError("k_out without k")
-    split, pair, batched, Hh, Wh = _rotation(d, split, pairing, positions, grid, B, N)
-    a = RopeArgs(_ptr(q), _ptr(q_out), _ptr(k), _ptr(k_out), q_st, qo_st, k_st, ko_st,
-                 _DTYPES[q.dtype], B, Hq, Hk, N, d, _ptr(positions), batched, Hh, Wh, int(offset),
-                 split, float(base), pair, inverse)
-    _check(lib.salad_rope(ctypes.byref(a), _stream(stream)), what)
+    else:
+        Hk, k_st, ko_st, kp, kop = 0, _NO_STRIDES, _NO_STRIDES, 0, 0
+    split, pair, at, batched, Hh, Wh = _rotation(d, split, pairing, positions, grid, B, N, dev)
+    a = _pack(_PACK_ROPE, what, q.data_ptr(), q_out.data_ptr(), kp, kop, *q_st, *qo_st, *k_st, *ko_st, code, B,
+              Hq, Hk, N, d, at, batched, Hh, Wh, offset, *split, base, pair, inverse)
+    _check(lib.salad_rope(a, _stream_on(stream, dev)), what)
     return q_out if k is None else (q_out, k_out)
 
 
@@ -539,8 +581,11 @@ class BlockCache:
         self.k_tail, self.v_tail, self.page_table = k_tail, v_tail, page_table
         self.B, self.H, self.d, self.pages, self.blocks = B, H, d, pages, blocks
         self.device = page_table.device
-        self.args = Cache(_ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(k_tail),
-                          _ptr(v_tail), _ptr(page_table), B, H, d, pages, blocks)
+        self.index = self.device.index
+        self.softmax_scale = 1.0 / math.sqrt(d)
+        # The fields of salad_cache, in order.
+        self.args = (_ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(k_tail),
+                     _ptr(v_tail), _ptr(page_table), B, H, d, pages, blocks)
 
     @classmethod
     def allocate(cls, B: int, H: int, d: int, blocks: int, *, pages: Optional[int] = None,
@@ -564,16 +609,14 @@ class BlockCache:
 
 
 def _cache_call(cache, seq, counts):
+    """(device index, address of seq, address of counts) of a call on a cache."""
     if not isinstance(cache, BlockCache):
         raise ValueError("cache must be a BlockCache")
-    if cache.device.index != torch.cuda.current_device():
-        raise ValueError(f"cache is on {cache.device}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    _shape(seq, (cache.B, 2), "seq")
-    _dev_tensor(seq, torch.int32, "seq")
-    if counts is not None:
-        _shape(counts, (cache.B,), "counts")
-        _dev_tensor(counts, torch.int32, "counts")
+    dev = torch.cuda.current_device()
+    if cache.index != dev:
+        raise ValueError(f"cache is on {cache.device}, but the current device is cuda:{dev}")
+    return (dev, _flat(seq, (cache.B, 2), torch.int32, dev, "seq"),
+            0 if counts is None else _flat(counts, (cache.B,), torch.int32, dev, "counts"))
 
 
 def cache_append(cache: BlockCache, k: torch.Tensor, v: torch.Tensor, seq: torch.Tensor, *,
@@ -592,24 +635,21 @@ def cache_append(cache: BlockCache, k: torch.Tensor, v: torch.Tensor, seq: torch
     ``seq`` (pages of blocks behind it are overwritten).
     """
     _dims(k, 4, "k", "[B, H, N, d]")
-    _cache_call(cache, seq, counts)
+    dev, seq_ptr, counts_ptr = _cache_call(cache, seq, counts)
     N = k.shape[2]
-    _shape(k, (cache.B, cache.H, N, cache.d), "k")
-    _shape(v, k.shape, "v")
-    k_st, v_st = _dev_rows(k, torch.bfloat16, "k"), _dev_rows(v, torch.bfloat16, "v")
-    rotate = int(positions is not None or grid is not None)
+    shape = (cache.B, cache.H, N, cache.d)
+    k_st, v_st = _rows(k, shape, torch.bfloat16, dev, "k"), _rows(v, shape, torch.bfloat16, dev, "v")
+    rotate = positions is not None or grid is not None
     if rotate:
-        split, pair, batched, Hh, Wh = _rotation(cache.d, split, pairing, positions, grid, cache.B, N)
+        split, pair, at, batched, Hh, Wh = _rotation(cache.d, split, pairing, positions, grid, cache.B, N, dev)
     else:
-        split, pair, batched, Hh, Wh = (0, 0, 0), 0, 0, 0, 0
+        split, pair, at, batched, Hh, Wh = _NO_STRIDES, 0, 0, 0, 0, 0
     if seq_out is None:
         seq_out = _empty_on(stream, lambda: torch.empty_like(seq))
-    else:
-        _shape(seq_out, seq.shape, "seq_out")
-        _dev_tensor(seq_out, torch.int32, "seq_out")
-    a = CacheAppendArgs(cache.args, _ptr(seq), _ptr(seq_out), _ptr(k), _ptr(v), k_st, v_st, N,
-                        _ptr(counts), rotate, _ptr(positions), batched, Hh, Wh, split, float(base), pair)
-    _check(lib.salad_cache_append(ctypes.byref(a), _stream(stream)), "salad_cache_append")
+    out_ptr = _flat(seq_out, (cache.B, 2), torch.int32, dev, "seq_out")
+    a = _pack(_PACK_APPEND, "salad_cache_append", *cache.args, seq_ptr, out_ptr, k.data_ptr(), v.data_ptr(), *k_st,
+              *v_st, N, counts_ptr, rotate, at, batched, Hh, Wh, *split, base, pair)
+    _check(lib.salad_cache_append(a, _stream_on(stream, dev)), "salad_cache_append")
     return seq_out
 
 
@@ -628,26 +668,22 @@ def cache_attn(cache: BlockCache, q: torch.Tensor, seq: torch.Tensor, *, counts=
     of the sum of exponentials.  Rows that see no key are 0, with lse = -inf.
     """
     _dims(q, 4, "q", "[B, H, N, d]")
-    _cache_call(cache, seq, counts)
-    B, Hq, N, d = q.shape
-    _shape(q, (cache.B, Hq, N, cache.d), "q")
-    q_st = _dev_rows(q, torch.bfloat16, "q")
+    dev, seq_ptr, counts_ptr = _cache_call(cache, seq, counts)
+    Hq, N = q.shape[1:3]
+    shape = (cache.B, Hq, N, cache.d)
+    q_st = _rows(q, shape, torch.bfloat16, dev, "q")
     if o is None:
         o = _empty_on(stream, lambda: torch.empty_like(q))
-    else:
-        _shape(o, q.shape, "o")
-    o_st = _dev_rows(o, torch.bfloat16, "o")
-    if lse is not None:
-        _shape(lse, (B, Hq, N), "lse")
-        _dev_tensor(lse, torch.float32, "lse")
-    a = CacheAttnArgs(cache.args, _ptr(seq), _ptr(q), _ptr(o), q_st, o_st, _ptr(lse), Hq, N,
-                      _ptr(counts), int(frame), int(window),
-                      1.0 / math.sqrt(d) if scale is None else float(scale), None, 0)
-    need = lib.salad_cache_attn_workspace_bytes(ctypes.byref(a))
+    o_st = _rows(o, shape, torch.bfloat16, dev, "o")
+    lse_ptr = 0 if lse is None else _flat(lse, shape[:3], torch.float32, dev, "lse")
+    head = (*cache.args, seq_ptr, q.data_ptr(), o.data_ptr(), *q_st, *o_st, lse_ptr, Hq, N, counts_ptr, frame,
+            window, cache.softmax_scale if scale is None else scale)
+    a = _pack(_PACK_ATTN, "salad_cache_attn", *head, 0, 0)
+    need = lib.salad_cache_attn_workspace_bytes(a)
     if need:
         ws = _empty_on(stream, lambda: _workspace(need, q.device, workspace))
-        a.workspace, a.workspace_bytes = _ptr(ws), ws.numel() * ws.element_size()
-    _check(lib.salad_cache_attn(ctypes.byref(a), _stream(stream)), "salad_cache_attn")
+        a = _PACK_ATTN.pack(*head, ws.data_ptr(), ws.numel() * ws.element_size())
+    _check(lib.salad_cache_attn(a, _stream_on(stream, dev)), "salad_cache_attn")
     return o
 
 
