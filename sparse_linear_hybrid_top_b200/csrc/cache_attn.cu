@@ -3,25 +3,29 @@
 //
 // Memory-bound: a query token reads every key and value of its sequence once,
 // 2 d bytes a token and head.  So the keys are split over as many warps as
-// fill the GPU, and every warp streams its own part from global memory to
-// registers with no shared-memory stage and no barrier in its loop: while one
-// half page (32 keys) is multiplied, the loads of the next one's keys and of
-// its own values are in flight (8 KB a warp at d = 128).  The products are
-// 16-row mma.sync tiles (query heads of a key head, and query tokens, fill
-// the rows); with so few rows the tensor pipe is far from its limit and
-// tcgen05's 128-row tiles would be mostly empty.
+// fill the GPU, and every key group (a warp, or the warps of 32 or 64 query
+// rows) streams its own part through a ring of half pages (32 keys, their
+// codes contiguous in a page: two bulk copies each) with its own barriers and
+// none across the CTA: 96 KB in flight per CTA, two CTAs per SM, where 45 KB
+// per SM cover the latency at the memory's rate.  The products are 16-row
+// mma.sync tiles (query heads of a key head, and query tokens, fill the rows);
+// with so few rows the tensor pipe is far from its limit and tcgen05's 128-row
+// tiles would be mostly empty.
 //
 // Both contractions are reordered so that a lane's 16-byte loads are its MMA
 // fragments.  QK: a lane holds 16 (32) consecutive channels of one key; MMA
-// step i multiplies channels {4i, 4i+2 | 4i+1, 4i+3} of each lane's run, and
+// step i multiplies channels {4i, 4i+1 | 4i+2, 4i+3} of each lane's run, and
 // the query fragments in shared memory are laid out the same way.  PV: a lane
 // holds 16 consecutive channels of four keys; column tile j is channels = j
 // mod 16, so lane group t ends with channels [32t, 32t+32) of its rows.
 //
-// Keys are multiplied as code values: their page's scale joins the softmax
-// scale.  Values too: a page's scale, a power of two, is added to the exponent
-// of its P (exact), and taken off the row sum again.  P is rounded to bf16
-// (half a step, 2^-8 of each weight); maxima, sums and O are float32.
+// Operands of closed blocks are fp16, in which a code is exact and converts in
+// one instruction per pair.  Key scales, and the power of two that brings a
+// query row into fp16's range, join the softmax scale.  P carries the power of
+// two of its value block and is kept against the largest product of weight and
+// scale, the row sum against the largest weight.  The open block is multiplied
+// in bf16 as it is held.  P is rounded to fp16 (2^-11 of each weight) or bf16
+// (2^-8); maxima, sums and O are float32.
 //
 // Partial results of the splits are merged by a second kernel, launched only
 // where there is more than one split.
@@ -41,6 +45,15 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 __device__ __forceinline__ uint32_t part(const uint4& v, int i) {
   return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w));
 }
@@ -51,21 +64,28 @@ struct Run;
 template <>
 struct Run<128> {
   uint4 v;
-  __device__ __forceinline__ void load(const unsigned char* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void load(const unsigned char* p) { v = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ uint32_t word(int i) const { return part(v, i); }
+  __device__ __forceinline__ void clear() { v = make_uint4(0u, 0u, 0u, 0u); }
 };
 template <>
 struct Run<64> {
   uint2 v;
-  __device__ __forceinline__ void load(const unsigned char* p) { v = __ldg(reinterpret_cast<const uint2*>(p)); }
+  __device__ __forceinline__ void load(const unsigned char* p) { v = *reinterpret_cast<const uint2*>(p); }
   __device__ __forceinline__ uint32_t word(int i) const { return i == 0 ? v.x : v.y; }
+  __device__ __forceinline__ void clear() { v = make_uint2(0u, 0u); }
 };
 
-__device__ __forceinline__ uint32_t finite_or_zero(uint32_t pair) {
-  if ((pair & 0x7f80u) == 0x7f80u) pair &= 0xffff0000u;
-  if ((pair & 0x7f800000u) == 0x7f800000u) pair &= 0xffffu;
-  return pair;
-}
+template <int D, int RW>
+struct Ring {
+  static constexpr int kGroups = 4 / RW;                 // key groups of a CTA
+  static constexpr int kHalf = 32 * D;                   // codes of 32 keys
+  // 80 KB with 64 query rows, whose fragments take 16 KB: two CTAs per SM.
+  static constexpr int kStages = (RW == 4 ? 80 : 96) * 1024 / (kGroups * 2 * kHalf);
+  static constexpr int kBytes = kGroups * kStages * 2 * kHalf;
+  static constexpr int kBars = kGroups * kStages * 2 * 8;
+  static constexpr int kSmem = kBytes + kBars;
+};
 
 // RW: warps over row tiles of 16; the other warps of the CTA split the keys.
 template <int D, int RW>
@@ -73,9 +93,14 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const __grid_const
   constexpr int KW = 4 / RW;           // warps over the keys
   constexpr int KS = D / 16;           // MMA steps of QK
   constexpr int NT = D / 8;            // column tiles of O
+  using R = Ring<D, RW>;
+  constexpr int NST = R::kStages;
+  extern __shared__ __align__(128) unsigned char ring[];     // [group][stage][K, V][32 keys][d]; then O, for the merge
+  auto os = reinterpret_cast<float (*)[KW][16][D + 4]>(ring);
+  static_assert(KW == 1 || RW * KW * 16 * (D + 4) * 4 <= R::kBytes, "the merge fits the ring");
   __shared__ uint4 qs[RW][KS][32];
-  __shared__ float os[KW > 1 ? RW : 1][KW > 1 ? KW : 1][16][D + 4];
   __shared__ float2 mls[RW][KW][16];
+  __shared__ uint32_t q_top[RW * 16];   // largest magnitude of a query row, as bf16 bits
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, t = lane % 4;
   const int rt = warp % RW, kw = warp / RW;
@@ -87,23 +112,58 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const __grid_const
   if (bad && threadIdx.x == 0) atomicOr(P.err, kErrRange);
   if (tile * RW * 16 >= count * P.group) return;      // no row of this tile exists
 
-  // Query fragments: entry (tile, step, lane) is the lane's A operand.
-  for (int e = threadIdx.x; e < RW * KS * 32; e += kThreads) {
-    const int l = e % 32, ks = (e / 32) % KS, w = e / (32 * KS);
+  // Query fragments: entry (tile, step, lane) is the lane's A operand, as fp16
+  // times a power of two that brings the row's largest magnitude into
+  // [2^14, 2^15) (a row with an infinity or a NaN stays as it is).
+  auto query = [&](int w, int ks, int l, int i) {
     const int c0 = (l % 4) * 16 + (ks % 4) * 4 + (ks / 4) * 64;
-    uint2 x[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = (tile * RW + w) * 16 + l / 4 + 8 * i;
-      const int n = r / P.group;
-      x[i] = make_uint2(0u, 0u);
-      if (n < count)
-        x[i] = *reinterpret_cast<const uint2*>(P.q + b * P.qb + (h * P.group + r % P.group) * P.qh + n * P.qn + 2 * c0);
+    const int r = (tile * RW + w) * 16 + l / 4 + 8 * i;
+    const int n = r / P.group;
+    if (n >= count) return make_uint2(0u, 0u);
+    return *reinterpret_cast<const uint2*>(P.q + b * P.qb + (h * P.group + r % P.group) * P.qh + n * P.qn + 2 * c0);
+  };
+  auto row_exponent = [&](int r) {
+    const uint32_t top = q_top[r];
+    const int e = top >= 0x7f80u ? 0 : static_cast<int>(top >> 7) - 127 - 14;
+    return e < -100 ? -100 : e;
+  };
+  constexpr int QE = RW * KS * 32 / kThreads;       // entries of a thread
+  uint2 qx[QE][2];
+  if (threadIdx.x < RW * 16) q_top[threadIdx.x] = 0;
+  // Barriers of a group's stage: landed, and free again (one arrival a warp).
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + R::kBytes);
+  auto landed = [&](int st) { return smem_u32(bars + (kw * NST + st) * 2); };
+  auto freed = [&](int st) { return smem_u32(bars + (kw * NST + st) * 2 + 1); };
+  if (rt == 0 && lane == 0) {
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(landed(i), 1);
+      mbar_init(freed(i), RW);
     }
-    qs[w][ks][l] = make_uint4(__byte_perm(x[0].x, x[0].y, 0x5410), __byte_perm(x[1].x, x[1].y, 0x5410),
-                              __byte_perm(x[0].x, x[0].y, 0x7632), __byte_perm(x[1].x, x[1].y, 0x7632));
+    fence_mbar_init();
   }
   __syncthreads();
+#pragma unroll
+  for (int x = 0; x < QE; ++x) {
+    const int e = threadIdx.x + x * kThreads, l = e % 32, w = e / (32 * KS);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      qx[x][i] = query(w, (e / 32) % KS, l, i);
+      const uint32_t top = __vmaxu2(qx[x][i].x & 0x7fff7fffu, qx[x][i].y & 0x7fff7fffu);
+      atomicMax(&q_top[w * 16 + l / 4 + 8 * i], max(top & 0xffffu, top >> 16));
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int x = 0; x < QE; ++x) {
+    const int e = threadIdx.x + x * kThreads, l = e % 32, w = e / (32 * KS);
+    const float f0 = __int_as_float((127 - row_exponent(w * 16 + l / 4)) << 23);
+    const float f1 = __int_as_float((127 - row_exponent(w * 16 + l / 4 + 8)) << 23);
+    qs[w][(e / 32) % KS][l] = make_uint4(bf16x2_to_f16x2(qx[x][0].x, f0), bf16x2_to_f16x2(qx[x][1].x, f1),
+                                         bf16x2_to_f16x2(qx[x][0].y, f0), bf16x2_to_f16x2(qx[x][1].y, f1));
+  }
+  __syncthreads();
+  const float q_factor[2] = {P.scale_log2 * __int_as_float((127 + row_exponent(rt * 16 + g)) << 23),
+                             P.scale_log2 * __int_as_float((127 + row_exponent(rt * 16 + g + 8)) << 23)};
 
   const int r0 = (tile * RW + rt) * 16;
   const CacheRow row[2] = {cache_row(P, r0 + g, h, s.len, count), cache_row(P, r0 + g + 8, h, s.len, count)};
@@ -128,10 +188,29 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const __grid_const
   for (int j = 0; j < NT; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[j][i] = 0.0f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+  // Of each row: the largest s + ev (s the base-2 score, ev the exponent of
+  // its value block's scale), the largest s, and the sum of 2^(s - ms).
+  float mt[2] = {-INFINITY, -INFINITY}, ms[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+  float ev_top = -INFINITY;
   bool vbad[2] = {false, false};
 
-  // This warp's half pages [u0, u1) of the tile's [lo, end).
+  // This group's half pages [u0, u1) of the CTA's [lo, end).
+  __shared__ int span[2];
+  if constexpr (RW > 1) {
+    // The group's warps walk over the same keys: those that any of them sees.
+    if (threadIdx.x == 0) {
+      span[0] = 0x7fffffff;
+      span[1] = 0;
+    }
+    __syncthreads();
+    if (lane == 0) {
+      atomicMin(&span[0], lo);
+      atomicMax(&span[1], end);
+    }
+    __syncthreads();
+    lo = span[0];
+    end = span[1];
+  }
   int u0 = 0, u1 = 0;
   if (end > 0) {
     const int h0 = lo / 32, nh = (end + 31) / 32 - h0;
@@ -141,16 +220,17 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const __grid_const
   }
   const int closed = 2 * (s.len / kCacheBlock);       // half pages of closed blocks
 
-  // One half page's softmax on S, the products of q with the code values: x =
-  // S * c2 in the base-2 domain; P, times 2^ev, back in sc.
-  auto softmax = [&](float (&sc)[4][4], int kbase, float c2, float ev, float inv_v, bool none) {
-    const bool partial = none || kbase < all_lo || kbase + 32 > all_end;
+  // One half page's softmax on S, the products of q with the code values: s =
+  // S * c2 in the base-2 domain; P = 2^(s + ev - mt) back in sc.
+  auto softmax = [&](float (&sc)[4][4], int kbase, float c20, float c21, float ev, bool odd, bool none) {
+    const bool partial = odd || kbase < all_lo || kbase + 32 > all_end;
+    const float c2[2] = {c20, c21};
     float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        sc[i][e] *= c2;
+        sc[i][e] *= c2[e >> 1];
         if (partial) {
           const int key = kbase + 8 * i + 2 * t + (e & 1);
           const CacheSpan& v = row[e >> 1].see;
@@ -163,67 +243,113 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const __grid_const
       top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
       top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
     }
-    float f[2], nm[2];
+    ev_top = fmaxf(ev_top, ev);
+    float f[2], nt[2], ns[2];
     bool grow = false;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float mn = fmaxf(m[i], top[i]);
-      grow = grow || mn > m[i];
-      f[i] = m[i] == -INFINITY ? 0.0f : ex2_ftz(m[i] - mn);
-      m[i] = mn;
-      // A row that has seen no key keeps m = -inf: exp2(-inf - 0) = 0.
-      nm[i] = mn == -INFINITY ? 0.0f : ev - mn;
+      const float tn = fmaxf(mt[i], top[i] + ev), sn = fmaxf(ms[i], top[i]);
+      grow = grow || tn > mt[i];
+      f[i] = mt[i] == -INFINITY ? 0.0f : ex2_ftz(mt[i] - tn);
+      if (sn > ms[i]) l[i] *= ex2_ftz(ms[i] - sn);
+      mt[i] = tn;
+      ms[i] = sn;
+      // A row that has seen no key keeps -inf: exp2(-inf - 0) = 0.
+      nt[i] = tn == -INFINITY ? 0.0f : -tn;
+      ns[i] = sn == -INFINITY ? 0.0f : -sn;
     }
     if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) l[i] *= f[i];
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[j][e] *= f[e >> 1];
+    }
+    if (ev_top - ev > 90.0f) {
+      // P may vanish beside another block's; the sum must not.
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          l[e >> 1] += ex2_ftz(sc[i][e] + ns[e >> 1]);
+          sc[i][e] = ex2_ftz(sc[i][e] + (nt[e >> 1] + ev));
+        }
+      return;
     }
     float sum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        sc[i][e] = ex2_ftz(sc[i][e] + nm[e >> 1]);
+        sc[i][e] = ex2_ftz(sc[i][e] + (nt[e >> 1] + ev));
         sum[e >> 1] += sc[i][e];
       }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) l[i] = fmaf(sum[i], inv_v, l[i]);
+    for (int i = 0; i < 2; ++i) l[i] = fmaf(sum[i], ex2_ftz(ns[i] - nt[i] - ev), l[i]);
   };
 
   // ---- closed blocks
   const int uc = min(u1, closed);
-  const unsigned char* kp = nullptr;
-  uint4 kr[4][D / 64];
-  Run<D> vr[2][4];
+  unsigned char* stages = ring + static_cast<size_t>(kw) * NST * 2 * R::kHalf;
   const int32_t* table = P.c.page_table + static_cast<long long>(b) * P.c.blocks;
-  int entry = u0 < uc ? __ldg(table + u0 / 2) : 0;
-  long long slab = 0;                  // page * H + head
-  float ks = 0.0f, vs = 0.0f;
-  bool none = false;
-  auto load_keys = [&](int u, int e) {
-    const int page = cache_page(e, P.c.pages);
-    none = page < 0;
-    slab = static_cast<long long>(none ? 0 : page) * P.c.H + h;
-    kp = P.c.k_pages + (slab * kCacheBlock + (u & 1) * 32 + g) * D + t * 16;
+  // Pages and scales of the 32 blocks from block `first` on, one per lane (-1:
+  // the entry is no page); the next 32 are loaded when these begin.
+  struct Blocks {
+    int page;
+    float ks, vs;
+  };
+  auto blocks_at = [&](int first) {
+    Blocks x{-1, 1.0f, 1.0f};
+    if (2 * (first + lane) < uc) {
+      x.page = cache_page(__ldg(table + first + lane), P.c.pages);
+      const long long at = static_cast<long long>(x.page < 0 ? 0 : x.page) * P.c.H + h;
+      x.ks = __ldg(P.c.k_scale + at);
+      x.vs = __ldg(P.c.v_scale + at);
+    }
+    return x;
+  };
+  const int b0 = u0 / 2;
+  Blocks cur = blocks_at(b0), nxt = blocks_at(b0 + 32);
+  // Half page u's copies (by the group's first warp); a block without a page
+  // reads page 0, and is masked.
+  auto fetch = [&](int u, const Blocks& x) {
+    const int page = __shfl_sync(0xffffffffu, x.page, (u / 2 - b0) % 32);
+    if (rt == 0 && lane == 0) {
+      const int st = (u - u0) % NST;
+      const long long at = (static_cast<long long>(page < 0 ? 0 : page) * P.c.H + h) * 2 + (u & 1);
+      const uint32_t dst = smem_u32(stages) + st * 2 * R::kHalf;
+      mbar_arrive_expect_tx(landed(st), 2 * R::kHalf);
+      bulk_load(dst, P.c.k_pages + at * R::kHalf, R::kHalf, landed(st));
+      bulk_load(dst + R::kHalf, P.c.v_pages + at * R::kHalf, R::kHalf, landed(st));
+    }
+  };
+  // Block groups of 32 that `cur` and `nxt` hold: in_cur is the first one's number.
+  int in_cur = 0;
+  auto blocks_of = [&](int u) -> const Blocks& { return (u / 2 - b0) / 32 == in_cur ? cur : nxt; };
+  static_assert(NST <= 62, "the ring stays within two groups of blocks");
+  int issued = u0;
+  for (; issued < uc && issued < u0 + NST; ++issued) fetch(issued, blocks_of(issued));
+  bool ok = true;
+  for (int u = u0; u < uc; ++u) {
+    const int st = (u - u0) % NST;
+    if ((u / 2 - b0) / 32 != in_cur) {
+      cur = nxt;
+      ++in_cur;
+      nxt = blocks_at(b0 + 32 * (in_cur + 1));
+    }
+    const int at = (u / 2 - b0) % 32;
+    const bool none = __shfl_sync(0xffffffffu, cur.page, at) < 0;
+    const float ks = __shfl_sync(0xffffffffu, cur.ks, at), vs = __shfl_sync(0xffffffffu, cur.vs, at);
+    if (!__all_sync(0xffffffffu, mbar_wait_poll(landed(st), static_cast<uint32_t>((u - u0) / NST) & 1u, P.wait_ns, nullptr))) {
+      ok = false;
+      break;
+    }
+    const unsigned char* kp = stages + st * 2 * R::kHalf + g * D + t * 16;
+    const unsigned char* vp = stages + st * 2 * R::kHalf + R::kHalf + 2 * t * D + g * (D / 8);
+    uint4 kr[4][D / 64];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int x = 0; x < D / 64; ++x) kr[i][x] = __ldg(reinterpret_cast<const uint4*>(kp + i * 8 * D + 64 * x));
-    ks = __ldg(P.c.k_scale + slab);
-    vs = __ldg(P.c.v_scale + slab);
-  };
-  if (u0 < uc) load_keys(u0, entry);
-  for (int u = u0; u < uc; ++u) {
-    const int next = u + 1 < uc ? __ldg(table + (u + 1) / 2) : 0;
-    const unsigned char* vp = P.c.v_pages + (slab * kCacheBlock + (u & 1) * 32 + 2 * t) * D + g * (D / 8);
-#pragma unroll
-    for (int st = 0; st < 2; ++st)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) vr[st][i].load(vp + (16 * st + (i & 1) + 8 * (i >> 1)) * D);
+      for (int x = 0; x < D / 64; ++x) kr[i][x] = *reinterpret_cast<const uint4*>(kp + i * 8 * D + 64 * x);
     float sc[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -234,63 +360,115 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const __grid_const
       const uint4 a = qs[rt][k][lane];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        uint32_t b0, b1;
-        e4m3_pairs(part(kr[i][k / 4], k % 4), b0, b1);
-        mma_bf16(sc[i], a.x, a.y, a.z, a.w, b0, b1);
+        const uint32_t w = part(kr[i][k / 4], k % 4);
+        mma_f16(sc[i], a.x, a.y, a.z, a.w, e4m3_to_f16x2(w), e4m3_to_f16x2(w >> 16));
       }
     }
-    const float c2 = P.scale_log2 * ks;
     const bool v_nan = isnan(vs);
-    const float ev = v_nan ? 0.0f : pow2_log(vs), inv_v = v_nan ? 1.0f : pow2_inv(vs);
-    const bool skip = none;
-    if (skip && lane == 0) atomicOr(P.err, kErrRange);
-    if (v_nan && !skip) {
+    const float ev = v_nan ? 0.0f : pow2_log(vs);
+    if (none && lane == 0) atomicOr(P.err, kErrRange);
+    softmax(sc, 32 * u, ks * q_factor[0], ks * q_factor[1], ev, none || isnan(ks), none);
+    Run<D> vr[2][4];
+#pragma unroll
+    for (int st2 = 0; st2 < 2; ++st2)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) vr[st2][i].load(vp + (16 * st2 + (i & 1) + 8 * (i >> 1)) * D);
+    if (v_nan || none) {
+      // The codes may be NaN: the rows that see them are marked instead.
+#pragma unroll
+      for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vr[st][i].clear();
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        vbad[i] = vbad[i] || (max(row[i].see.lo, 32 * u) < min(row[i].see.end, 32 * u + 32));
+        vbad[i] = vbad[i] || (!none && max(row[i].see.lo, 32 * u) < min(row[i].see.end, 32 * u + 32));
     }
-    if (u + 1 < uc) load_keys(u + 1, next);
-    softmax(sc, 32 * u, c2, ev, inv_v, skip);
+    // The stage is read: it can be filled again, by the group's first warp once
+    // every warp of the group says so.
+    __syncwarp();
+    if (RW > 1 && lane == 0) mbar_arrive(freed(st));
+    if (issued < uc) {
+      if (RW > 1 && rt == 0 &&
+          !__all_sync(0xffffffffu, mbar_wait_poll(freed(st), static_cast<uint32_t>((u - u0) / NST) & 1u, P.wait_ns, nullptr))) {
+        ok = false;
+        break;
+      }
+      fetch(issued, blocks_of(issued));
+      ++issued;
+    }
 #pragma unroll
     for (int st = 0; st < 2; ++st) {
-      const uint32_t a0 = pack_bf16x2(sc[2 * st][0], sc[2 * st][1]), a1 = pack_bf16x2(sc[2 * st][2], sc[2 * st][3]);
-      const uint32_t a2 = pack_bf16x2(sc[2 * st + 1][0], sc[2 * st + 1][1]);
-      const uint32_t a3 = pack_bf16x2(sc[2 * st + 1][2], sc[2 * st + 1][3]);
+      const uint32_t a0 = pack_f16x2(sc[2 * st][0], sc[2 * st][1]), a1 = pack_f16x2(sc[2 * st][2], sc[2 * st][3]);
+      const uint32_t a2 = pack_f16x2(sc[2 * st + 1][0], sc[2 * st + 1][1]);
+      const uint32_t a3 = pack_f16x2(sc[2 * st + 1][2], sc[2 * st + 1][3]);
 #pragma unroll
       for (int w = 0; w < D / 32; ++w) {
-        uint32_t lo0, lo1, hi0, hi1, lo2, lo3, hi2, hi3;
-        e4m3_pairs(__byte_perm(vr[st][0].word(w), vr[st][1].word(w), 0x5410), lo0, lo1);
-        e4m3_pairs(__byte_perm(vr[st][0].word(w), vr[st][1].word(w), 0x7632), lo2, lo3);
-        e4m3_pairs(__byte_perm(vr[st][2].word(w), vr[st][3].word(w), 0x5410), hi0, hi1);
-        e4m3_pairs(__byte_perm(vr[st][2].word(w), vr[st][3].word(w), 0x7632), hi2, hi3);
-        mma_bf16(o[4 * w], a0, a1, a2, a3, lo0, hi0);
-        mma_bf16(o[4 * w + 1], a0, a1, a2, a3, lo1, hi1);
-        mma_bf16(o[4 * w + 2], a0, a1, a2, a3, lo2, hi2);
-        mma_bf16(o[4 * w + 3], a0, a1, a2, a3, lo3, hi3);
+        // Channels 0, 1 and 2, 3 of two keys each: (key, next key) pairs.
+        const uint32_t x0 = __byte_perm(vr[st][0].word(w), vr[st][1].word(w), 0x5140);
+        const uint32_t x1 = __byte_perm(vr[st][0].word(w), vr[st][1].word(w), 0x7362);
+        const uint32_t y0 = __byte_perm(vr[st][2].word(w), vr[st][3].word(w), 0x5140);
+        const uint32_t y1 = __byte_perm(vr[st][2].word(w), vr[st][3].word(w), 0x7362);
+        mma_f16(o[4 * w], a0, a1, a2, a3, e4m3_to_f16x2(x0), e4m3_to_f16x2(y0));
+        mma_f16(o[4 * w + 1], a0, a1, a2, a3, e4m3_to_f16x2(x0 >> 16), e4m3_to_f16x2(y0 >> 16));
+        mma_f16(o[4 * w + 2], a0, a1, a2, a3, e4m3_to_f16x2(x1), e4m3_to_f16x2(y1));
+        mma_f16(o[4 * w + 3], a0, a1, a2, a3, e4m3_to_f16x2(x1 >> 16), e4m3_to_f16x2(y1 >> 16));
       }
     }
   }
 
-  // ---- the open block, in bf16 (at most two half pages of one warp)
-  for (int u = max(u0, closed); u < u1; ++u) {
+  if (!ok) atomicOr(P.err, kErrTimeout);
+  // No copy may be in flight when the ring is used again, or at the exit: each
+  // one issued is waited for here, unless the loop above has seen it land.
+  if (!ok && rt == 0)
+    for (int u = max(u0, issued - NST); u < issued; ++u)
+      mbar_wait_poll(landed((u - u0) % NST), static_cast<uint32_t>((u - u0) / NST) & 1u, P.wait_ns, nullptr);
+
+  // ---- the open block, in bf16 (at most two half pages of one group).  All
+  // loads of a half page are issued before the first is used.
+  for (int u = max(u0, closed); u < u1 && ok; ++u) {
     const long long at = (((static_cast<long long>(b) * 2 + s.slot) * P.c.H + h) * kCacheBlock + (u & 1) * 32) * D;
     const __nv_bfloat16* kt = static_cast<const __nv_bfloat16*>(P.c.k_tail) + at;
     const __nv_bfloat16* vt = static_cast<const __nv_bfloat16*>(P.c.v_tail) + at;
+    // 16-channel runs of a key as two 16-byte loads, as queries and keys have
+    // them; of a value 16 (8 at d = 64) channels of four keys a step.
+    uint4 kx[4][D / 64][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int x = 0; x < D / 64; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          kx[i][x][y] = __ldg(reinterpret_cast<const uint4*>(kt + (8 * i + g) * D + 64 * x + 16 * t + 8 * y));
     float sc[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) sc[i][e] = 0.0f;
+    {
+      uint2 qt[KS][2];
 #pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      const uint4 a = qs[rt][k][lane];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint2 x = *reinterpret_cast<const uint2*>(kt + (8 * i + g) * D + t * 16 + (k % 4) * 4 + (k / 4) * 64);
-        mma_bf16(sc[i], a.x, a.y, a.z, a.w, __byte_perm(x.x, x.y, 0x5410), __byte_perm(x.x, x.y, 0x7632));
+      for (int k = 0; k < KS; ++k) {
+        qt[k][0] = query(rt, k, lane, 0);
+        qt[k][1] = query(rt, k, lane, 1);
       }
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4& x = kx[i][k / 4][(k % 4) / 2];
+          mma_bf16(sc[i], qt[k][0].x, qt[k][1].x, qt[k][0].y, qt[k][1].y, part(x, 2 * (k % 2)), part(x, 2 * (k % 2) + 1));
+        }
     }
-    softmax(sc, 32 * u, P.scale_log2, 0.0f, 1.0f, false);
+    uint4 vx[2][4][D / 64];
+#pragma unroll
+    for (int st = 0; st < 2; ++st)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int y = 0; y < D / 64; ++y)
+          vx[st][i][y] = __ldg(reinterpret_cast<const uint4*>(
+              vt + (16 * st + 2 * t + (i & 1) + 8 * (i >> 1)) * D + g * (D / 8) + 8 * y));
+    softmax(sc, 32 * u, P.scale_log2, P.scale_log2, 0.0f, false, false);
     bool odd = false;                  // a value that is not finite
 #pragma unroll
     for (int st = 0; st < 2; ++st) {
@@ -302,8 +480,7 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const __grid_const
         uint32_t x[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t y = *reinterpret_cast<const uint32_t*>(
-              vt + (16 * st + 2 * t + (i & 1) + 8 * (i >> 1)) * D + g * (D / 8) + 2 * w);
+          const uint32_t y = part(vx[st][i][w / 4], w % 4);
           x[i] = finite_or_zero(y);
           odd = odd || x[i] != y;
         }
@@ -331,10 +508,12 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const __grid_const
   for (int i = 0; i < 2; ++i) {
     l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
     l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-    if (vbad[i]) {
+    // O in units of 2^ms, like the sum.
+    const float unit = mt[i] == -INFINITY ? 1.0f : ex2_ftz(mt[i] - ms[i]);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) o[j][2 * i] = o[j][2 * i + 1] = __int_as_float(0x7fffffff);
-    }
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) o[j][2 * i + e] = vbad[i] ? __int_as_float(0x7fffffff) : o[j][2 * i + e] * unit;
   }
 
   // ---- merge the CTA's key warps, then write the rows (or their part)
@@ -372,9 +551,10 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const __grid_const
         acc[j] = o[j][2 * i];
         acc[NT + j] = o[j][2 * i + 1];
       }
-      put(rt * 16 + g + 8 * i, acc, m[i], l[i], t * (D / 4), D / 4);
+      put(rt * 16 + g + 8 * i, acc, ms[i], l[i], t * (D / 4), D / 4);
     }
   } else {
+    __syncthreads();                 // every group is done with the ring
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
 #pragma unroll
@@ -384,7 +564,7 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const __grid_const
         *reinterpret_cast<float4*>(&os[rt][kw][g + 8 * i][t * (D / 4) + NT + j]) =
             make_float4(o[j][2 * i + 1], o[j + 1][2 * i + 1], o[j + 2][2 * i + 1], o[j + 3][2 * i + 1]);
       }
-      if (t == 0) mls[rt][kw][g + 8 * i] = make_float2(m[i], l[i]);
+      if (t == 0) mls[rt][kw][g + 8 * i] = make_float2(ms[i], l[i]);
     }
     __syncthreads();
     for (int e = threadIdx.x; e < RW * 16 * (D / 8); e += kThreads) {
@@ -423,20 +603,39 @@ __global__ void __launch_bounds__(kThreads) cache_merge_kernel(const __grid_cons
   const int count = P.counts == nullptr ? P.N : cache_count(__ldg(P.counts + b), P.N, &bad);
   const int n = r / P.group, head = h * P.group + r % P.group;
   if (n >= count) return;
-  float mm = -INFINITY;
-  for (int k = lane; k < P.splits; k += 32) mm = fmaxf(mm, P.part_ml[k * rows + at].x);
+  // A split a lane (two past 32): its weight against the largest maximum, 0
+  // where it saw no key (its O is 0 too).
+  float2 p[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    p[i] = lane + 32 * i < P.splits ? P.part_ml[(lane + 32 * i) * rows + at] : make_float2(-INFINITY, 0.0f);
+  float mm = fmaxf(p[0].x, p[1].x);
 #pragma unroll
   for (int i = 16; i > 0; i /= 2) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, i));
-  constexpr int C = D / 32;
-  float ll = 0.0f, acc[C] = {};
-  for (int k = 0; k < P.splits; ++k) {
-    const float2 p = P.part_ml[k * rows + at];
-    if (p.y == 0.0f) continue;
-    const float f = p.x == -INFINITY ? 1.0f : ex2_ftz(p.x - mm);
-    ll = fmaf(p.y, f, ll);
-    const float* from = P.part_o + (k * rows + at) * D + lane * C;
+  float w[2], ll = 0.0f;
 #pragma unroll
-    for (int c = 0; c < C; ++c) acc[c] = fmaf(from[c], f, acc[c]);
+  for (int i = 0; i < 2; ++i) {
+    w[i] = p[i].y == 0.0f ? 0.0f : (p[i].x == -INFINITY ? 1.0f : ex2_ftz(p[i].x - mm));
+    ll = fmaf(p[i].y, w[i], ll);
+  }
+#pragma unroll
+  for (int i = 16; i > 0; i /= 2) ll += __shfl_xor_sync(0xffffffffu, ll, i);
+  constexpr int C = D / 32;
+  float acc[C] = {};
+  const float* from = P.part_o + at * D + lane * C;
+  // Eight splits' loads in flight.
+  for (int k0 = 0; k0 < P.splits; k0 += 8) {
+    float v[8][C];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int c = 0; c < C; ++c) v[i][c] = k0 + i < P.splits ? from[(k0 + i) * rows * D + c] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float f = __shfl_sync(0xffffffffu, k0 < 32 ? w[0] : w[1], (k0 + i) % 32);
+#pragma unroll
+      for (int c = 0; c < C; ++c) acc[c] = fmaf(v[i][c], f, acc[c]);
+    }
   }
   const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
   char* to = P.o + b * P.ob + head * P.oh + n * P.on + 2 * lane * C;
@@ -459,10 +658,10 @@ Shape shape_of(const CacheAttnArgs& a, int num_sms) {
   s.tiles = static_cast<int>((rows + s.rw * 16 - 1) / (s.rw * 16));
   const long long bh = static_cast<long long>(a.cache.B) * a.cache.H;
   s.rows = bh * s.tiles * s.rw * 16;
-  // Enough CTAs for three on every SM, each key warp with two half pages at
-  // the least (of a full table).
+  // One wave of CTAs, two to an SM, and two half pages to a key group at the
+  // least (of a full table).
   const long long ctas = bh * s.tiles;
-  long long splits = (3ll * num_sms + ctas - 1) / ctas;
+  long long splits = 2ll * num_sms / ctas;
   const long long most = (a.cache.blocks + 1ll) * 2 / (2 * (4 / s.rw));
   if (splits > most) splits = most;
   if (splits > 64) splits = 64;
@@ -470,13 +669,19 @@ Shape shape_of(const CacheAttnArgs& a, int num_sms) {
   return s;
 }
 
+template <int D, int RW>
+cudaError_t launch_rw(const Ctx& c, const CacheAttnParams& P, const Shape& s) {
+  const dim3 grid(static_cast<unsigned>(s.tiles) * s.splits, P.c.B * P.c.H);
+  const cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D, RW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             Ring<D, RW>::kSmem);
+  if (e != cudaSuccess) return e;
+  cache_attn_kernel<D, RW><<<grid, kThreads, Ring<D, RW>::kSmem, c.stream>>>(P);
+  return cudaGetLastError();
+}
+
 template <int D>
 cudaError_t launch_d(const Ctx& c, const CacheAttnParams& P, const Shape& s) {
-  const dim3 grid(static_cast<unsigned>(s.tiles) * s.splits, P.c.B * P.c.H);
-  if (s.rw == 1) cache_attn_kernel<D, 1><<<grid, kThreads, 0, c.stream>>>(P);
-  else if (s.rw == 2) cache_attn_kernel<D, 2><<<grid, kThreads, 0, c.stream>>>(P);
-  else cache_attn_kernel<D, 4><<<grid, kThreads, 0, c.stream>>>(P);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = s.rw == 1 ? launch_rw<D, 1>(c, P, s) : (s.rw == 2 ? launch_rw<D, 2>(c, P, s) : launch_rw<D, 4>(c, P, s));
   if (e != cudaSuccess || s.splits == 1) return e;
   cache_merge_kernel<D><<<static_cast<unsigned>((s.rows + 3) / 4), kThreads, 0, c.stream>>>(P, s.rw * 16);
   return cudaGetLastError();

@@ -1,6 +1,8 @@
 // cache_attn.cuh -- what the two attention kernels over the 8-bit block cache
-// share: e4m3 codes as bf16 pairs, and the parameters.
+// share: e4m3 codes as fp16 pairs, and the parameters.
 #pragma once
+
+#include <cuda_fp16.h>
 
 #include "cache_index.h"
 #include "common.cuh"
@@ -27,20 +29,41 @@ struct CacheAttnParams {
   unsigned long long wait_ns;
 };
 
-// Four e4m3 codes as two bf16 pairs: even = (byte 0, byte 2), odd = (byte 1,
-// byte 3).  A code's seven magnitude bits, put at bit 4 of a bf16, are its
-// value times 2^-120 for normals and subnormals alike (the exponent biases
-// are 7 and 127), so one exact multiplication by 2^120 finishes it.  The code
-// of NaN comes out as 480: a block that holds one has a NaN scale.
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+// Two e4m3 codes as fp16 (exact).
+__device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t codes) {
   uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<unsigned short>(codes)));
   return r;
 }
-__device__ __forceinline__ void e4m3_pairs(uint32_t w, uint32_t& even, uint32_t& odd) {
-  constexpr uint32_t kMag = 0x07f007f0u, kSign = 0x80008000u, k2p120 = 0x7b807b80u;
-  even = mul_bf16x2(((w << 4) & kMag) | ((w << 8) & kSign), k2p120);
-  odd = mul_bf16x2(((w >> 4) & kMag) | (w & kSign), k2p120);
+__device__ __forceinline__ uint4 eight_codes(uint2 c) {
+  return make_uint4(e4m3_to_f16x2(c.x), e4m3_to_f16x2(c.x >> 16), e4m3_to_f16x2(c.y), e4m3_to_f16x2(c.y >> 16));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// bf16 pairs times a power of two as fp16.
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t x, float factor) {
+  const float2 f = unpack_bf16x2(x);
+  return pack_f16x2(f.x * factor, f.y * factor);
+}
+__device__ __forceinline__ uint4 scaled_f16(uint4 x, float factor) {
+  return make_uint4(bf16x2_to_f16x2(x.x, factor), bf16x2_to_f16x2(x.y, factor), bf16x2_to_f16x2(x.z, factor),
+                    bf16x2_to_f16x2(x.w, factor));
+}
+
+__device__ __forceinline__ uint32_t finite_or_zero(uint32_t pair) {
+  if ((pair & 0x7f80u) == 0x7f80u) pair &= 0xffff0000u;
+  if ((pair & 0x7f800000u) == 0x7f800000u) pair &= 0xffffu;
+  return pair;
+}
+
+// Untiled bulk copy global -> shared completing on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
 }
 
 __device__ __forceinline__ float ex2_ftz(float x) {

@@ -37,7 +37,6 @@
 // holds whole is written at once; the others leave float32 parts (two per
 // CTA at most), merged by a last launch.
 #include <cstring>
-#include <cuda_fp16.h>
 
 #include "cache_attn.cuh"
 
@@ -264,29 +263,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// Two e4m3 codes as fp16 (exact).
-__device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t codes) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<unsigned short>(codes)));
-  return r;
-}
-__device__ __forceinline__ uint4 eight_codes(uint2 c) {
-  return make_uint4(e4m3_to_f16x2(c.x), e4m3_to_f16x2(c.x >> 16), e4m3_to_f16x2(c.y), e4m3_to_f16x2(c.y >> 16));
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-// bf16 pairs times a power of two as fp16.
-__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t x, float factor) {
-  const float2 f = unpack_bf16x2(x);
-  return pack_f16x2(f.x * factor, f.y * factor);
-}
-__device__ __forceinline__ uint4 scaled_f16(uint4 x, float factor) {
-  return make_uint4(bf16x2_to_f16x2(x.x, factor), bf16x2_to_f16x2(x.y, factor), bf16x2_to_f16x2(x.z, factor),
-                    bf16x2_to_f16x2(x.w, factor));
-}
-
 // Asynchronous TMEM load of 64 columns; the registers hold it after tmem_arrived.
 __device__ __forceinline__ void tmem_ld64_async(uint32_t taddr, uint32_t* r) {
   asm volatile(
@@ -326,26 +302,12 @@ __device__ __forceinline__ void pin32(uint32_t* r) {
   asm volatile("" : SALAD_RW8(r, 16), SALAD_RW8(r, 24));
 }
 
-// Untiled bulk copy global -> shared completing on `bar`.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
-
 // The power of two that brings magnitudes up to bf16 bits `top` (finite) to
 // at most 448: a closed block's rule.
 __device__ __forceinline__ float tail_scale(uint32_t top) {
   int e = static_cast<int>(top >> 7) - 127 - 8 + ((top & 127u) > 96u ? 1 : 0);
   e = e < -100 ? -100 : e;
   return __int_as_float((127 + e) << 23);
-}
-
-__device__ __forceinline__ uint32_t finite_or_zero(uint32_t pair) {
-  if ((pair & 0x7f80u) == 0x7f80u) pair &= 0xffff0000u;
-  if ((pair & 0x7f800000u) == 0x7f800000u) pair &= 0xffffu;
-  return pair;
 }
 
 template <int D>
@@ -1043,11 +1005,12 @@ __global__ void __launch_bounds__(256) cache_tc_merge_kernel(const __grid_consta
     for (int c = c0; c <= c1; ++c)
       m = fmaxf(m, P.part_ml[(2ll * c + (c == c0 ? first_part : 0)) * kRows + r].x);
     float l = 0.0f, acc[C] = {};
+#pragma unroll 4
     for (int c = c0; c <= c1; ++c) {
       const long long at = (2ll * c + (c == c0 ? first_part : 0)) * kRows + r;
       const float2 p = P.part_ml[at];
-      if (p.y == 0.0f) continue;
-      const float f = p.x == -INFINITY ? 1.0f : ex2_ftz(p.x - m);
+      // A part that saw no key has a sum of 0 (and an O of 0).
+      const float f = p.y == 0.0f ? 0.0f : (p.x == -INFINITY ? 1.0f : ex2_ftz(p.x - m));
       l = fmaf(p.y, f, l);
       const float* from = P.part_o + at * D + lane * C;
 #pragma unroll
