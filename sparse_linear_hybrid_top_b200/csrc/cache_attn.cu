@@ -27,8 +27,11 @@
 // in bf16 as it is held.  P is rounded to fp16 (2^-11 of each weight) or bf16
 // (2^-8); maxima, sums and O are float32.
 //
-// Partial results of the splits are merged by a second kernel, launched only
-// where there is more than one split.
+// Balance: lengths are known on the device only and differ in a batch.  Every
+// CTA sums them (up to 512 sequences) and takes an equal run of a head's half
+// pages, which may begin and end inside a sequence; its key groups share each
+// sequence's part of the run.  A sequence that one CTA holds whole is written at
+// once, the parts of the others are merged by a second launch.
 #include "cache_attn.cuh"
 
 namespace salad {
@@ -87,49 +90,58 @@ struct Ring {
   static constexpr int kSmem = kBytes + kBars;
 };
 
+constexpr int kScan = 512;             // sequences that a CTA sums
+
+struct SeqSpan {
+  int len, slot, count;
+  int first, n;                        // half pages that the query rows see; n >= 1 where there is a row
+};
+__device__ __forceinline__ SeqSpan seq_span(const CacheAttnParams& P, int b, bool* bad) {
+  const CacheSeq s = cache_seq(__ldg(P.seq + 2 * b), __ldg(P.seq + 2 * b + 1), P.c.blocks, bad);
+  SeqSpan x{s.len, s.slot, P.counts == nullptr ? P.N : cache_count(__ldg(P.counts + b), P.N, bad), 0, 0};
+  if (x.count == 0) return x;
+  // lo and end grow with the row.
+  const int lo = cache_visible(x.len - x.count, x.len, x.count, P.frame, P.window).lo;
+  const int end = cache_visible(x.len - 1, x.len, x.count, P.frame, P.window).end;
+  x.n = 1;
+  if (end > lo) {
+    x.first = lo / 32;
+    x.n = (end + 31) / 32 - x.first;
+  }
+  return x;
+}
+
+// CTAs of a head that share `total` half pages: two half pages to a key group
+// at the least.
+__device__ __forceinline__ long long run_ctas(long long total, int slots) {
+  const long long most = (total + 7) / 8;
+  return most < slots ? (most < 1 ? 1 : most) : slots;
+}
+
 // RW: warps over row tiles of 16; the other warps of the CTA split the keys.
 template <int D, int RW>
 __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const __grid_constant__ CacheAttnParams P) {
-  constexpr int KW = 4 / RW;           // warps over the keys
+  constexpr int KW = 4 / RW;           // key groups
   constexpr int KS = D / 16;           // MMA steps of QK
   constexpr int NT = D / 8;            // column tiles of O
+  constexpr int ROWS = RW * 16;
   using R = Ring<D, RW>;
   constexpr int NST = R::kStages;
-  extern __shared__ __align__(128) unsigned char ring[];     // [group][stage][K, V][32 keys][d]; then O, for the merge
+  extern __shared__ __align__(128) unsigned char ring[];     // [group][stage][K, V][32 keys][d]; O, for the merge
   auto os = reinterpret_cast<float (*)[KW][16][D + 4]>(ring);
   static_assert(KW == 1 || RW * KW * 16 * (D + 4) * 4 <= R::kBytes, "the merge fits the ring");
   __shared__ uint4 qs[RW][KS][32];
   __shared__ float2 mls[RW][KW][16];
-  __shared__ uint32_t q_top[RW * 16];   // largest magnitude of a query row, as bf16 bits
+  __shared__ uint32_t q_top[ROWS];     // largest magnitude of a query row, as bf16 bits
+  __shared__ long long plan[kScan + 1];
+  __shared__ long long warp_sum[4];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, t = lane % 4;
   const int rt = warp % RW, kw = warp / RW;
-  const int tile = blockIdx.x / P.splits, split = blockIdx.x % P.splits;
-  const int b = blockIdx.y / P.c.H, h = blockIdx.y % P.c.H;
-  bool bad = false;
-  const CacheSeq s = cache_seq(__ldg(P.seq + 2 * b), __ldg(P.seq + 2 * b + 1), P.c.blocks, &bad);
-  const int count = P.counts == nullptr ? P.N : cache_count(__ldg(P.counts + b), P.N, &bad);
-  if (bad && threadIdx.x == 0) atomicOr(P.err, kErrRange);
-  if (tile * RW * 16 >= count * P.group) return;      // no row of this tile exists
+  const int h = blockIdx.y;
+  // The second launch's CTAs may take their places as this one's leave them.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // Query fragments: entry (tile, step, lane) is the lane's A operand, as fp16
-  // times a power of two that brings the row's largest magnitude into
-  // [2^14, 2^15) (a row with an infinity or a NaN stays as it is).
-  auto query = [&](int w, int ks, int l, int i) {
-    const int c0 = (l % 4) * 16 + (ks % 4) * 4 + (ks / 4) * 64;
-    const int r = (tile * RW + w) * 16 + l / 4 + 8 * i;
-    const int n = r / P.group;
-    if (n >= count) return make_uint2(0u, 0u);
-    return *reinterpret_cast<const uint2*>(P.q + b * P.qb + (h * P.group + r % P.group) * P.qh + n * P.qn + 2 * c0);
-  };
-  auto row_exponent = [&](int r) {
-    const uint32_t top = q_top[r];
-    const int e = top >= 0x7f80u ? 0 : static_cast<int>(top >> 7) - 127 - 14;
-    return e < -100 ? -100 : e;
-  };
-  constexpr int QE = RW * KS * 32 / kThreads;       // entries of a thread
-  uint2 qx[QE][2];
-  if (threadIdx.x < RW * 16) q_top[threadIdx.x] = 0;
   // Barriers of a group's stage: landed, and free again (one arrival a warp).
   uint64_t* bars = reinterpret_cast<uint64_t*>(ring + R::kBytes);
   auto landed = [&](int st) { return smem_u32(bars + (kw * NST + st) * 2); };
@@ -141,480 +153,548 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const __grid_const
     }
     fence_mbar_init();
   }
-  __syncthreads();
+  // Prefix sums of the sequences' half pages, and this CTA's run [w0, w1).
+  const bool scan = P.c.B <= kScan;
+  int b = blockIdx.x, b_end = b + 1;
+  long long w0 = 0, w1 = 0x7fffffffffffffffll;
+  if (scan) {
+    long long sum = 0;
+    for (int b0 = 0; b0 < P.c.B; b0 += kThreads) {
+      const int i = b0 + threadIdx.x;
+      bool bad = false;
+      long long x = i < P.c.B ? seq_span(P, i, &bad).n : 0;
+      if (bad && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(P.err, kErrRange);
+      const long long own = x;
 #pragma unroll
-  for (int x = 0; x < QE; ++x) {
-    const int e = threadIdx.x + x * kThreads, l = e % 32, w = e / (32 * KS);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      qx[x][i] = query(w, (e / 32) % KS, l, i);
-      const uint32_t top = __vmaxu2(qx[x][i].x & 0x7fff7fffu, qx[x][i].y & 0x7fff7fffu);
-      atomicMax(&q_top[w * 16 + l / 4 + 8 * i], max(top & 0xffffu, top >> 16));
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int x = 0; x < QE; ++x) {
-    const int e = threadIdx.x + x * kThreads, l = e % 32, w = e / (32 * KS);
-    const float f0 = __int_as_float((127 - row_exponent(w * 16 + l / 4)) << 23);
-    const float f1 = __int_as_float((127 - row_exponent(w * 16 + l / 4 + 8)) << 23);
-    qs[w][(e / 32) % KS][l] = make_uint4(bf16x2_to_f16x2(qx[x][0].x, f0), bf16x2_to_f16x2(qx[x][1].x, f1),
-                                         bf16x2_to_f16x2(qx[x][0].y, f0), bf16x2_to_f16x2(qx[x][1].y, f1));
-  }
-  __syncthreads();
-  const float q_factor[2] = {P.scale_log2 * __int_as_float((127 + row_exponent(rt * 16 + g)) << 23),
-                             P.scale_log2 * __int_as_float((127 + row_exponent(rt * 16 + g + 8)) << 23)};
-
-  const int r0 = (tile * RW + rt) * 16;
-  const CacheRow row[2] = {cache_row(P, r0 + g, h, s.len, count), cache_row(P, r0 + g + 8, h, s.len, count)};
-  // Keys that any row of the tile sees, and keys that every row sees.
-  int lo = 0x7fffffff, end = 0, all_lo = 0, all_end = 0x7fffffff;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if (row[i].see.end > 0) lo = min(lo, row[i].see.lo);
-    end = max(end, row[i].see.end);
-    if (row[i].valid) {
-      all_lo = max(all_lo, row[i].see.lo);
-      all_end = min(all_end, row[i].see.end);
-    }
-  }
-  lo = __reduce_min_sync(0xffffffffu, lo);
-  end = __reduce_max_sync(0xffffffffu, end);
-  all_lo = __reduce_max_sync(0xffffffffu, all_lo);
-  all_end = __reduce_min_sync(0xffffffffu, all_end);
-
-  float o[NT][4];
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[j][i] = 0.0f;
-  // Of each row: the largest s + ev (s the base-2 score, ev the exponent of
-  // its value block's scale), the largest s, and the sum of 2^(s - ms).
-  float mt[2] = {-INFINITY, -INFINITY}, ms[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-  float ev_top = -INFINITY;
-  bool vbad[2] = {false, false};
-
-  // This group's half pages [u0, u1) of the CTA's [lo, end).
-  __shared__ int span[2];
-  if constexpr (RW > 1) {
-    // The group's warps walk over the same keys: those that any of them sees.
-    if (threadIdx.x == 0) {
-      span[0] = 0x7fffffff;
-      span[1] = 0;
-    }
-    __syncthreads();
-    if (lane == 0) {
-      atomicMin(&span[0], lo);
-      atomicMax(&span[1], end);
-    }
-    __syncthreads();
-    lo = span[0];
-    end = span[1];
-  }
-  int u0 = 0, u1 = 0;
-  if (end > 0) {
-    const int h0 = lo / 32, nh = (end + 31) / 32 - h0;
-    const int u = split * KW + kw, U = P.splits * KW;
-    u0 = h0 + static_cast<int>(static_cast<long long>(nh) * u / U);
-    u1 = h0 + static_cast<int>(static_cast<long long>(nh) * (u + 1) / U);
-  }
-  const int closed = 2 * (s.len / kCacheBlock);       // half pages of closed blocks
-
-  // One half page's softmax on S, the products of q with the code values: s =
-  // S * c2 in the base-2 domain; P = 2^(s + ev - mt) back in sc.
-  auto softmax = [&](float (&sc)[4][4], int kbase, float c20, float c21, float ev, bool odd, bool none) {
-    const bool partial = odd || kbase < all_lo || kbase + 32 > all_end;
-    const float c2[2] = {c20, c21};
-    float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        sc[i][e] *= c2[e >> 1];
-        if (partial) {
-          const int key = kbase + 8 * i + 2 * t + (e & 1);
-          const CacheSpan& v = row[e >> 1].see;
-          if (none || key < v.lo || key >= v.end) sc[i][e] = -INFINITY;
-        }
-        top[e >> 1] = fmaxf(top[e >> 1], sc[i][e]);
+      for (int d = 1; d < 32; d *= 2) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
       }
+      if (lane == 31) warp_sum[warp] = x;
+      __syncthreads();
+      long long before = sum;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k < warp) before += warp_sum[k];
+        sum += warp_sum[k];
+      }
+      if (i < P.c.B) plan[i] = before + x - own;
+      __syncthreads();
+    }
+    if (threadIdx.x == 0) plan[P.c.B] = sum;
+    __syncthreads();
+    const long long ctas = run_ctas(sum, gridDim.x);
+    if (blockIdx.x == 0 && h == 0 && P.plan != nullptr)
+      for (int i = threadIdx.x; i <= P.c.B; i += kThreads) P.plan[i] = plan[i];
+    if (blockIdx.x >= ctas) return;
+    w0 = sum * blockIdx.x / ctas;
+    w1 = sum * (blockIdx.x + 1) / ctas;
+    int lo = 0, hi = P.c.B;            // plan[lo] <= w0 < plan[hi], the last such lo
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (plan[mid] <= w0) lo = mid; else hi = mid;
+    }
+    b = lo;
+    b_end = P.c.B;
+  } else {
+    __syncthreads();                   // the barriers
+  }
+  int done = 0;                        // half pages of this group's ring so far
+  bool ok = true;
+  for (; b < b_end && (!scan || plan[b] < w1); ++b) {
+    bool bad = false;                    // reported above, or by the sequence's own CTA
+    const SeqSpan s = seq_span(P, b, &bad);
+    if (bad && !scan && threadIdx.x == 0 && h == 0) atomicOr(P.err, kErrRange);
+    if (s.n == 0) continue;
+    const int count = s.count;
+    const long long from_b = scan ? plan[b] : 0;
+    const int part0 = w0 > from_b ? static_cast<int>(w0 - from_b) : 0;
+    const int part1 = w1 - from_b < s.n ? static_cast<int>(w1 - from_b) : s.n;
+    const bool whole = part0 == 0 && part1 == s.n;
+
+    // This group's half pages [u0, u1): its share of the CTA's part.
+    const int u0 = s.first + part0 + (part1 - part0) * kw / KW;
+    const int u1 = s.first + part0 + (part1 - part0) * (kw + 1) / KW;
+    const int closed = 2 * (s.len / kCacheBlock);       // half pages of closed blocks
+    const int uc = min(u1, closed);
+    unsigned char* stages = ring + static_cast<size_t>(kw) * NST * 2 * R::kHalf;
+    const int32_t* table = P.c.page_table + static_cast<long long>(b) * P.c.blocks;
+    // Pages and scales of the 32 blocks from block `first` on, one per lane (-1:
+    // the entry is no page); the next 32 are loaded when these begin.
+    struct Blocks {
+      int page;
+      float ks, vs;
+    };
+    auto blocks_at = [&](int first) {
+      Blocks x{-1, 1.0f, 1.0f};
+      if (2 * (first + lane) < uc) {
+        x.page = cache_page(__ldg(table + first + lane), P.c.pages);
+        const long long at = static_cast<long long>(x.page < 0 ? 0 : x.page) * P.c.H + h;
+        x.ks = __ldg(P.c.k_scale + at);
+        x.vs = __ldg(P.c.v_scale + at);
+      }
+      return x;
+    };
+    const int b0 = u0 / 2;
+    Blocks cur = blocks_at(b0), nxt = blocks_at(b0 + 32);
+
+    // Query fragments: entry (tile, step, lane) is the lane's A operand, as fp16
+    // times a power of two that brings the row's largest magnitude into
+    // [2^14, 2^15) (a row with an infinity or a NaN stays as it is).
+    auto query = [&](int w, int ks, int l, int i) {
+      const int c0 = (l % 4) * 16 + (ks % 4) * 4 + (ks / 4) * 64;
+      const int r = w * 16 + l / 4 + 8 * i;
+      const int n = r / P.group;
+      if (n >= count) return make_uint2(0u, 0u);
+      return *reinterpret_cast<const uint2*>(P.q + b * P.qb + (h * P.group + r % P.group) * P.qh + n * P.qn + 2 * c0);
+    };
+    auto row_exponent = [&](int r) {
+      const uint32_t top = q_top[r];
+      const int e = top >= 0x7f80u ? 0 : static_cast<int>(top >> 7) - 127 - 14;
+      return e < -100 ? -100 : e;
+    };
+    constexpr int QE = RW * KS * 32 / kThreads;       // entries of a thread
+    uint2 qx[QE][2];
+#pragma unroll
+    for (int x = 0; x < QE; ++x) {
+      const int e = threadIdx.x + x * kThreads, l = e % 32, w = e / (32 * KS);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) qx[x][i] = query(w, (e / 32) % KS, l, i);
+    }
+    if (threadIdx.x < ROWS) q_top[threadIdx.x] = 0;
+    // Half page u's copies (by the group's first warp); a block without a page
+    // reads page 0, and is masked.
+    auto fetch = [&](int u, const Blocks& x) {
+      const int page = __shfl_sync(0xffffffffu, x.page, (u / 2 - b0) % 32);
+      if (rt == 0 && lane == 0) {
+        const int st = (done + u - u0) % NST;
+        const long long at = (static_cast<long long>(page < 0 ? 0 : page) * P.c.H + h) * 2 + (u & 1);
+        const uint32_t dst = smem_u32(stages) + st * 2 * R::kHalf;
+        mbar_arrive_expect_tx(landed(st), 2 * R::kHalf);
+        bulk_load(dst, P.c.k_pages + at * R::kHalf, R::kHalf, landed(st));
+        bulk_load(dst + R::kHalf, P.c.v_pages + at * R::kHalf, R::kHalf, landed(st));
+      }
+    };
+    // Block groups of 32 that `cur` and `nxt` hold: in_cur is the first one's number.
+    int in_cur = 0;
+    auto blocks_of = [&](int u) -> const Blocks& { return (u / 2 - b0) / 32 == in_cur ? cur : nxt; };
+    static_assert(NST <= 62, "the ring stays within two groups of blocks");
+    int issued = u0;
+    for (; issued < uc && issued < u0 + NST; ++issued) fetch(issued, blocks_of(issued));
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < QE; ++x) {
+      const int e = threadIdx.x + x * kThreads, l = e % 32, w = e / (32 * KS);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t top = __vmaxu2(qx[x][i].x & 0x7fff7fffu, qx[x][i].y & 0x7fff7fffu);
+        atomicMax(&q_top[w * 16 + l / 4 + 8 * i], max(top & 0xffffu, top >> 16));
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < QE; ++x) {
+      const int e = threadIdx.x + x * kThreads, l = e % 32, w = e / (32 * KS);
+      const float f0 = __int_as_float((127 - row_exponent(w * 16 + l / 4)) << 23);
+      const float f1 = __int_as_float((127 - row_exponent(w * 16 + l / 4 + 8)) << 23);
+      qs[w][(e / 32) % KS][l] = make_uint4(bf16x2_to_f16x2(qx[x][0].x, f0), bf16x2_to_f16x2(qx[x][1].x, f1),
+                                           bf16x2_to_f16x2(qx[x][0].y, f0), bf16x2_to_f16x2(qx[x][1].y, f1));
+    }
+    __syncthreads();
+    const float q_factor[2] = {P.scale_log2 * __int_as_float((127 + row_exponent(rt * 16 + g)) << 23),
+                               P.scale_log2 * __int_as_float((127 + row_exponent(rt * 16 + g + 8)) << 23)};
+
+    const int r0 = rt * 16;
+    const CacheRow row[2] = {cache_row(P, r0 + g, h, s.len, count), cache_row(P, r0 + g + 8, h, s.len, count)};
+    // Keys that every row of the tile sees.
+    int all_lo = 0, all_end = 0x7fffffff;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
-      top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+      if (row[i].valid) {
+        all_lo = max(all_lo, row[i].see.lo);
+        all_end = min(all_end, row[i].see.end);
+      }
     }
-    ev_top = fmaxf(ev_top, ev);
-    float f[2], nt[2], ns[2];
-    bool grow = false;
+    all_lo = __reduce_max_sync(0xffffffffu, all_lo);
+    all_end = __reduce_min_sync(0xffffffffu, all_end);
+
+    float o[NT][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float tn = fmaxf(mt[i], top[i] + ev), sn = fmaxf(ms[i], top[i]);
-      grow = grow || tn > mt[i];
-      f[i] = mt[i] == -INFINITY ? 0.0f : ex2_ftz(mt[i] - tn);
-      if (sn > ms[i]) l[i] *= ex2_ftz(ms[i] - sn);
-      mt[i] = tn;
-      ms[i] = sn;
-      // A row that has seen no key keeps -inf: exp2(-inf - 0) = 0.
-      nt[i] = tn == -INFINITY ? 0.0f : -tn;
-      ns[i] = sn == -INFINITY ? 0.0f : -sn;
-    }
-    if (__any_sync(0xffffffffu, grow)) {
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[j][e] *= f[e >> 1];
-    }
-    if (ev_top - ev > 90.0f) {
-      // P may vanish beside another block's; the sum must not.
+      for (int i = 0; i < 4; ++i) o[j][i] = 0.0f;
+    // Of each row: the largest s + ev (s the base-2 score, ev the exponent of
+    // its value block's scale), the largest s, and the sum of 2^(s - ms).
+    float mt[2] = {-INFINITY, -INFINITY}, ms[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    float ev_top = -INFINITY;
+    bool vbad[2] = {false, false};
+
+    // One half page's softmax on S, the products of q with the code values: s =
+    // S * c2 in the base-2 domain; P = 2^(s + ev - mt) back in sc.
+    auto softmax = [&](float (&sc)[4][4], int kbase, float c20, float c21, float ev, bool odd, bool none) {
+      const bool partial = odd || kbase < all_lo || kbase + 32 > all_end;
+      const float c2[2] = {c20, c21};
+      float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          l[e >> 1] += ex2_ftz(sc[i][e] + ns[e >> 1]);
-          sc[i][e] = ex2_ftz(sc[i][e] + (nt[e >> 1] + ev));
+          sc[i][e] *= c2[e >> 1];
+          if (partial) {
+            const int key = kbase + 8 * i + 2 * t + (e & 1);
+            const CacheSpan& v = row[e >> 1].see;
+            if (none || key < v.lo || key >= v.end) sc[i][e] = -INFINITY;
+          }
+          top[e >> 1] = fmaxf(top[e >> 1], sc[i][e]);
         }
-      return;
-    }
-    float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        sc[i][e] = ex2_ftz(sc[i][e] + (nt[e >> 1] + ev));
-        sum[e >> 1] += sc[i][e];
+      for (int i = 0; i < 2; ++i) {
+        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
       }
+      ev_top = fmaxf(ev_top, ev);
+      float f[2], nt[2], ns[2];
+      bool grow = false;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) l[i] = fmaf(sum[i], ex2_ftz(ns[i] - nt[i] - ev), l[i]);
-  };
-
-  // ---- closed blocks
-  const int uc = min(u1, closed);
-  unsigned char* stages = ring + static_cast<size_t>(kw) * NST * 2 * R::kHalf;
-  const int32_t* table = P.c.page_table + static_cast<long long>(b) * P.c.blocks;
-  // Pages and scales of the 32 blocks from block `first` on, one per lane (-1:
-  // the entry is no page); the next 32 are loaded when these begin.
-  struct Blocks {
-    int page;
-    float ks, vs;
-  };
-  auto blocks_at = [&](int first) {
-    Blocks x{-1, 1.0f, 1.0f};
-    if (2 * (first + lane) < uc) {
-      x.page = cache_page(__ldg(table + first + lane), P.c.pages);
-      const long long at = static_cast<long long>(x.page < 0 ? 0 : x.page) * P.c.H + h;
-      x.ks = __ldg(P.c.k_scale + at);
-      x.vs = __ldg(P.c.v_scale + at);
-    }
-    return x;
-  };
-  const int b0 = u0 / 2;
-  Blocks cur = blocks_at(b0), nxt = blocks_at(b0 + 32);
-  // Half page u's copies (by the group's first warp); a block without a page
-  // reads page 0, and is masked.
-  auto fetch = [&](int u, const Blocks& x) {
-    const int page = __shfl_sync(0xffffffffu, x.page, (u / 2 - b0) % 32);
-    if (rt == 0 && lane == 0) {
-      const int st = (u - u0) % NST;
-      const long long at = (static_cast<long long>(page < 0 ? 0 : page) * P.c.H + h) * 2 + (u & 1);
-      const uint32_t dst = smem_u32(stages) + st * 2 * R::kHalf;
-      mbar_arrive_expect_tx(landed(st), 2 * R::kHalf);
-      bulk_load(dst, P.c.k_pages + at * R::kHalf, R::kHalf, landed(st));
-      bulk_load(dst + R::kHalf, P.c.v_pages + at * R::kHalf, R::kHalf, landed(st));
-    }
-  };
-  // Block groups of 32 that `cur` and `nxt` hold: in_cur is the first one's number.
-  int in_cur = 0;
-  auto blocks_of = [&](int u) -> const Blocks& { return (u / 2 - b0) / 32 == in_cur ? cur : nxt; };
-  static_assert(NST <= 62, "the ring stays within two groups of blocks");
-  int issued = u0;
-  for (; issued < uc && issued < u0 + NST; ++issued) fetch(issued, blocks_of(issued));
-  bool ok = true;
-  for (int u = u0; u < uc; ++u) {
-    const int st = (u - u0) % NST;
-    if ((u / 2 - b0) / 32 != in_cur) {
-      cur = nxt;
-      ++in_cur;
-      nxt = blocks_at(b0 + 32 * (in_cur + 1));
-    }
-    const int at = (u / 2 - b0) % 32;
-    const bool none = __shfl_sync(0xffffffffu, cur.page, at) < 0;
-    const float ks = __shfl_sync(0xffffffffu, cur.ks, at), vs = __shfl_sync(0xffffffffu, cur.vs, at);
-    if (!__all_sync(0xffffffffu, mbar_wait_poll(landed(st), static_cast<uint32_t>((u - u0) / NST) & 1u, P.wait_ns, nullptr))) {
-      ok = false;
-      break;
-    }
-    const unsigned char* kp = stages + st * 2 * R::kHalf + g * D + t * 16;
-    const unsigned char* vp = stages + st * 2 * R::kHalf + R::kHalf + 2 * t * D + g * (D / 8);
-    uint4 kr[4][D / 64];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int x = 0; x < D / 64; ++x) kr[i][x] = *reinterpret_cast<const uint4*>(kp + i * 8 * D + 64 * x);
-    float sc[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sc[i][e] = 0.0f;
-#pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      const uint4 a = qs[rt][k][lane];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t w = part(kr[i][k / 4], k % 4);
-        mma_f16(sc[i], a.x, a.y, a.z, a.w, e4m3_to_f16x2(w), e4m3_to_f16x2(w >> 16));
+      for (int i = 0; i < 2; ++i) {
+        const float tn = fmaxf(mt[i], top[i] + ev), sn = fmaxf(ms[i], top[i]);
+        grow = grow || tn > mt[i];
+        f[i] = mt[i] == -INFINITY ? 0.0f : ex2_ftz(mt[i] - tn);
+        if (sn > ms[i]) l[i] *= ex2_ftz(ms[i] - sn);
+        mt[i] = tn;
+        ms[i] = sn;
+        // A row that has seen no key keeps -inf: exp2(-inf - 0) = 0.
+        nt[i] = tn == -INFINITY ? 0.0f : -tn;
+        ns[i] = sn == -INFINITY ? 0.0f : -sn;
       }
-    }
-    const bool v_nan = isnan(vs);
-    const float ev = v_nan ? 0.0f : pow2_log(vs);
-    if (none && lane == 0) atomicOr(P.err, kErrRange);
-    softmax(sc, 32 * u, ks * q_factor[0], ks * q_factor[1], ev, none || isnan(ks), none);
-    Run<D> vr[2][4];
-#pragma unroll
-    for (int st2 = 0; st2 < 2; ++st2)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) vr[st2][i].load(vp + (16 * st2 + (i & 1) + 8 * (i >> 1)) * D);
-    if (v_nan || none) {
-      // The codes may be NaN: the rows that see them are marked instead.
-#pragma unroll
-      for (int st = 0; st < 2; ++st)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) vr[st][i].clear();
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        vbad[i] = vbad[i] || (!none && max(row[i].see.lo, 32 * u) < min(row[i].see.end, 32 * u + 32));
-    }
-    // The stage is read: it can be filled again, by the group's first warp once
-    // every warp of the group says so.
-    __syncwarp();
-    if (RW > 1 && lane == 0) mbar_arrive(freed(st));
-    if (issued < uc) {
-      if (RW > 1 && rt == 0 &&
-          !__all_sync(0xffffffffu, mbar_wait_poll(freed(st), static_cast<uint32_t>((u - u0) / NST) & 1u, P.wait_ns, nullptr))) {
-        ok = false;
-        break;
-      }
-      fetch(issued, blocks_of(issued));
-      ++issued;
-    }
-#pragma unroll
-    for (int st = 0; st < 2; ++st) {
-      const uint32_t a0 = pack_f16x2(sc[2 * st][0], sc[2 * st][1]), a1 = pack_f16x2(sc[2 * st][2], sc[2 * st][3]);
-      const uint32_t a2 = pack_f16x2(sc[2 * st + 1][0], sc[2 * st + 1][1]);
-      const uint32_t a3 = pack_f16x2(sc[2 * st + 1][2], sc[2 * st + 1][3]);
-#pragma unroll
-      for (int w = 0; w < D / 32; ++w) {
-        // Channels 0, 1 and 2, 3 of two keys each: (key, next key) pairs.
-        const uint32_t x0 = __byte_perm(vr[st][0].word(w), vr[st][1].word(w), 0x5140);
-        const uint32_t x1 = __byte_perm(vr[st][0].word(w), vr[st][1].word(w), 0x7362);
-        const uint32_t y0 = __byte_perm(vr[st][2].word(w), vr[st][3].word(w), 0x5140);
-        const uint32_t y1 = __byte_perm(vr[st][2].word(w), vr[st][3].word(w), 0x7362);
-        mma_f16(o[4 * w], a0, a1, a2, a3, e4m3_to_f16x2(x0), e4m3_to_f16x2(y0));
-        mma_f16(o[4 * w + 1], a0, a1, a2, a3, e4m3_to_f16x2(x0 >> 16), e4m3_to_f16x2(y0 >> 16));
-        mma_f16(o[4 * w + 2], a0, a1, a2, a3, e4m3_to_f16x2(x1), e4m3_to_f16x2(y1));
-        mma_f16(o[4 * w + 3], a0, a1, a2, a3, e4m3_to_f16x2(x1 >> 16), e4m3_to_f16x2(y1 >> 16));
-      }
-    }
-  }
-
-  if (!ok) atomicOr(P.err, kErrTimeout);
-  // No copy may be in flight when the ring is used again, or at the exit: each
-  // one issued is waited for here, unless the loop above has seen it land.
-  if (!ok && rt == 0)
-    for (int u = max(u0, issued - NST); u < issued; ++u)
-      mbar_wait_poll(landed((u - u0) % NST), static_cast<uint32_t>((u - u0) / NST) & 1u, P.wait_ns, nullptr);
-
-  // ---- the open block, in bf16 (at most two half pages of one group).  All
-  // loads of a half page are issued before the first is used.
-  for (int u = max(u0, closed); u < u1 && ok; ++u) {
-    const long long at = (((static_cast<long long>(b) * 2 + s.slot) * P.c.H + h) * kCacheBlock + (u & 1) * 32) * D;
-    const __nv_bfloat16* kt = static_cast<const __nv_bfloat16*>(P.c.k_tail) + at;
-    const __nv_bfloat16* vt = static_cast<const __nv_bfloat16*>(P.c.v_tail) + at;
-    // 16-channel runs of a key as two 16-byte loads, as queries and keys have
-    // them; of a value 16 (8 at d = 64) channels of four keys a step.
-    uint4 kx[4][D / 64][2];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int x = 0; x < D / 64; ++x)
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-          kx[i][x][y] = __ldg(reinterpret_cast<const uint4*>(kt + (8 * i + g) * D + 64 * x + 16 * t + 8 * y));
-    float sc[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sc[i][e] = 0.0f;
-    {
-      uint2 qt[KS][2];
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        qt[k][0] = query(rt, k, lane, 0);
-        qt[k][1] = query(rt, k, lane, 1);
-      }
-#pragma unroll
-      for (int k = 0; k < KS; ++k)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4& x = kx[i][k / 4][(k % 4) / 2];
-          mma_bf16(sc[i], qt[k][0].x, qt[k][1].x, qt[k][0].y, qt[k][1].y, part(x, 2 * (k % 2)), part(x, 2 * (k % 2) + 1));
-        }
-    }
-    uint4 vx[2][4][D / 64];
-#pragma unroll
-    for (int st = 0; st < 2; ++st)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int y = 0; y < D / 64; ++y)
-          vx[st][i][y] = __ldg(reinterpret_cast<const uint4*>(
-              vt + (16 * st + 2 * t + (i & 1) + 8 * (i >> 1)) * D + g * (D / 8) + 8 * y));
-    softmax(sc, 32 * u, P.scale_log2, P.scale_log2, 0.0f, false, false);
-    bool odd = false;                  // a value that is not finite
-#pragma unroll
-    for (int st = 0; st < 2; ++st) {
-      const uint32_t a0 = pack_bf16x2(sc[2 * st][0], sc[2 * st][1]), a1 = pack_bf16x2(sc[2 * st][2], sc[2 * st][3]);
-      const uint32_t a2 = pack_bf16x2(sc[2 * st + 1][0], sc[2 * st + 1][1]);
-      const uint32_t a3 = pack_bf16x2(sc[2 * st + 1][2], sc[2 * st + 1][3]);
-#pragma unroll
-      for (int w = 0; w < D / 16; ++w) {
-        uint32_t x[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t y = part(vx[st][i][w / 4], w % 4);
-          x[i] = finite_or_zero(y);
-          odd = odd || x[i] != y;
-        }
-        mma_bf16(o[2 * w], a0, a1, a2, a3, __byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410));
-        mma_bf16(o[2 * w + 1], a0, a1, a2, a3, __byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632));
-      }
-    }
-    // Infinities and NaN reach only the rows that see their key (they would
-    // spread as 0 * inf through the product).
-    if (__any_sync(0xffffffffu, odd)) {
-      for (int key = 0; key < 32; ++key) {
+      if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
+          for (int e = 0; e < 4; ++e) o[j][e] *= f[e >> 1];
+      }
+      if (ev_top - ev > 90.0f) {
+        // P may vanish beside another block's; the sum must not.
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float v = __bfloat162float(vt[key * D + (D / 4) * t + (D / 8) * (e & 1) + j]);
-            const CacheSpan& see = row[e >> 1].see;
-            if (!isfinite(v) && 32 * u + key >= see.lo && 32 * u + key < see.end) o[j][e] += v;
+            l[e >> 1] += ex2_ftz(sc[i][e] + ns[e >> 1]);
+            sc[i][e] = ex2_ftz(sc[i][e] + (nt[e >> 1] + ev));
+          }
+        return;
+      }
+      float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sc[i][e] = ex2_ftz(sc[i][e] + (nt[e >> 1] + ev));
+          sum[e >> 1] += sc[i][e];
+        }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) l[i] = fmaf(sum[i], ex2_ftz(ns[i] - nt[i] - ev), l[i]);
+    };
+
+    // ---- closed blocks
+    for (int u = u0; u < uc; ++u) {
+      const int st = (done + u - u0) % NST;
+      if ((u / 2 - b0) / 32 != in_cur) {
+        cur = nxt;
+        ++in_cur;
+        nxt = blocks_at(b0 + 32 * (in_cur + 1));
+      }
+      const int at = (u / 2 - b0) % 32;
+      const bool none = __shfl_sync(0xffffffffu, cur.page, at) < 0;
+      const float ks = __shfl_sync(0xffffffffu, cur.ks, at), vs = __shfl_sync(0xffffffffu, cur.vs, at);
+      if (!__all_sync(0xffffffffu, mbar_wait_poll(landed(st), static_cast<uint32_t>((done + u - u0) / NST) & 1u, P.wait_ns, nullptr))) {
+        ok = false;
+        break;
+      }
+      const unsigned char* kp = stages + st * 2 * R::kHalf + g * D + t * 16;
+      const unsigned char* vp = stages + st * 2 * R::kHalf + R::kHalf + 2 * t * D + g * (D / 8);
+      uint4 kr[4][D / 64];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) kr[i][x] = *reinterpret_cast<const uint4*>(kp + i * 8 * D + 64 * x);
+      float sc[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[i][e] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const uint4 a = qs[rt][k][lane];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w = part(kr[i][k / 4], k % 4);
+          mma_f16(sc[i], a.x, a.y, a.z, a.w, e4m3_to_f16x2(w), e4m3_to_f16x2(w >> 16));
+        }
+      }
+      const bool v_nan = isnan(vs);
+      const float ev = v_nan ? 0.0f : pow2_log(vs);
+      if (none && lane == 0) atomicOr(P.err, kErrRange);
+      softmax(sc, 32 * u, ks * q_factor[0], ks * q_factor[1], ev, none || isnan(ks), none);
+      Run<D> vr[2][4];
+#pragma unroll
+      for (int st2 = 0; st2 < 2; ++st2)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vr[st2][i].load(vp + (16 * st2 + (i & 1) + 8 * (i >> 1)) * D);
+      if (v_nan || none) {
+        // The codes may be NaN: the rows that see them are marked instead.
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) vr[st][i].clear();
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          vbad[i] = vbad[i] || (!none && max(row[i].see.lo, 32 * u) < min(row[i].see.end, 32 * u + 32));
+      }
+      // The stage is read: it can be filled again, by the group's first warp once
+      // every warp of the group says so.
+      __syncwarp();
+      if (RW > 1 && lane == 0) mbar_arrive(freed(st));
+      if (issued < uc) {
+        if (RW > 1 && rt == 0 &&
+            !__all_sync(0xffffffffu, mbar_wait_poll(freed(st), static_cast<uint32_t>((done + u - u0) / NST) & 1u, P.wait_ns, nullptr))) {
+          ok = false;
+          break;
+        }
+        fetch(issued, blocks_of(issued));
+        ++issued;
+      }
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        const uint32_t a0 = pack_f16x2(sc[2 * st][0], sc[2 * st][1]), a1 = pack_f16x2(sc[2 * st][2], sc[2 * st][3]);
+        const uint32_t a2 = pack_f16x2(sc[2 * st + 1][0], sc[2 * st + 1][1]);
+        const uint32_t a3 = pack_f16x2(sc[2 * st + 1][2], sc[2 * st + 1][3]);
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+          // Channels 0, 1 and 2, 3 of two keys each: (key, next key) pairs.
+          const uint32_t x0 = __byte_perm(vr[st][0].word(w), vr[st][1].word(w), 0x5140);
+          const uint32_t x1 = __byte_perm(vr[st][0].word(w), vr[st][1].word(w), 0x7362);
+          const uint32_t y0 = __byte_perm(vr[st][2].word(w), vr[st][3].word(w), 0x5140);
+          const uint32_t y1 = __byte_perm(vr[st][2].word(w), vr[st][3].word(w), 0x7362);
+          mma_f16(o[4 * w], a0, a1, a2, a3, e4m3_to_f16x2(x0), e4m3_to_f16x2(y0));
+          mma_f16(o[4 * w + 1], a0, a1, a2, a3, e4m3_to_f16x2(x0 >> 16), e4m3_to_f16x2(y0 >> 16));
+          mma_f16(o[4 * w + 2], a0, a1, a2, a3, e4m3_to_f16x2(x1), e4m3_to_f16x2(y1));
+          mma_f16(o[4 * w + 3], a0, a1, a2, a3, e4m3_to_f16x2(x1 >> 16), e4m3_to_f16x2(y1 >> 16));
+        }
+      }
+    }
+
+    if (!ok) atomicOr(P.err, kErrTimeout);
+    // No copy may be in flight when the ring is used again, or at the exit: each
+    // one issued is waited for here, unless the loop above has seen it land.
+    if (!ok && rt == 0)
+      for (int u = max(u0, issued - NST); u < issued; ++u)
+        mbar_wait_poll(landed((done + u - u0) % NST), static_cast<uint32_t>((done + u - u0) / NST) & 1u, P.wait_ns, nullptr);
+    done += max(0, uc - u0);
+
+    // ---- the open block, in bf16 (at most two half pages of one group).  All
+    // loads of a half page are issued before the first is used.
+    for (int u = max(u0, closed); u < u1 && ok; ++u) {
+      const long long at = (((static_cast<long long>(b) * 2 + s.slot) * P.c.H + h) * kCacheBlock + (u & 1) * 32) * D;
+      const __nv_bfloat16* kt = static_cast<const __nv_bfloat16*>(P.c.k_tail) + at;
+      const __nv_bfloat16* vt = static_cast<const __nv_bfloat16*>(P.c.v_tail) + at;
+      // 16-channel runs of a key as two 16-byte loads, as queries and keys have
+      // them; of a value 16 (8 at d = 64) channels of four keys a step.
+      uint4 kx[4][D / 64][2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x)
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+            kx[i][x][y] = __ldg(reinterpret_cast<const uint4*>(kt + (8 * i + g) * D + 64 * x + 16 * t + 8 * y));
+      float sc[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[i][e] = 0.0f;
+      {
+        uint2 qt[KS][2];
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          qt[k][0] = query(rt, k, lane, 0);
+          qt[k][1] = query(rt, k, lane, 1);
+        }
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4& x = kx[i][k / 4][(k % 4) / 2];
+            mma_bf16(sc[i], qt[k][0].x, qt[k][1].x, qt[k][0].y, qt[k][1].y, part(x, 2 * (k % 2)), part(x, 2 * (k % 2) + 1));
           }
       }
+      uint4 vx[2][4][D / 64];
+#pragma unroll
+      for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int y = 0; y < D / 64; ++y)
+            vx[st][i][y] = __ldg(reinterpret_cast<const uint4*>(
+                vt + (16 * st + 2 * t + (i & 1) + 8 * (i >> 1)) * D + g * (D / 8) + 8 * y));
+      softmax(sc, 32 * u, P.scale_log2, P.scale_log2, 0.0f, false, false);
+      bool odd = false;                  // a value that is not finite
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        const uint32_t a0 = pack_bf16x2(sc[2 * st][0], sc[2 * st][1]), a1 = pack_bf16x2(sc[2 * st][2], sc[2 * st][3]);
+        const uint32_t a2 = pack_bf16x2(sc[2 * st + 1][0], sc[2 * st + 1][1]);
+        const uint32_t a3 = pack_bf16x2(sc[2 * st + 1][2], sc[2 * st + 1][3]);
+#pragma unroll
+        for (int w = 0; w < D / 16; ++w) {
+          uint32_t x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t y = part(vx[st][i][w / 4], w % 4);
+            x[i] = finite_or_zero(y);
+            odd = odd || x[i] != y;
+          }
+          mma_bf16(o[2 * w], a0, a1, a2, a3, __byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410));
+          mma_bf16(o[2 * w + 1], a0, a1, a2, a3, __byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632));
+        }
+      }
+      // Infinities and NaN reach only the rows that see their key (they would
+      // spread as 0 * inf through the product).
+      if (__any_sync(0xffffffffu, odd)) {
+        for (int key = 0; key < 32; ++key) {
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float v = __bfloat162float(vt[key * D + (D / 4) * t + (D / 8) * (e & 1) + j]);
+              const CacheSpan& see = row[e >> 1].see;
+              if (!isfinite(v) && 32 * u + key >= see.lo && 32 * u + key < see.end) o[j][e] += v;
+            }
+        }
+      }
     }
-  }
 
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-    // O in units of 2^ms, like the sum.
-    const float unit = mt[i] == -INFINITY ? 1.0f : ex2_ftz(mt[i] - ms[i]);
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      // O in units of 2^ms, like the sum.
+      const float unit = mt[i] == -INFINITY ? 1.0f : ex2_ftz(mt[i] - ms[i]);
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) o[j][2 * i + e] = vbad[i] ? __int_as_float(0x7fffffff) : o[j][2 * i + e] * unit;
-  }
+        for (int e = 0; e < 2; ++e) o[j][2 * i + e] = vbad[i] ? __int_as_float(0x7fffffff) : o[j][2 * i + e] * unit;
+    }
 
-  // ---- merge the CTA's key warps, then write the rows (or their part)
-  const long long rows = static_cast<long long>(gridDim.y) * P.tiles * (RW * 16);
-  auto put = [&](int r, const float* acc, float mm, float ll, int c0, int nc) {
-    // acc: nc channels from c0 of row r of this tile, unnormalised.
-    const CacheRow x = cache_row(P, tile * RW * 16 + r, h, s.len, count);
-    if (!x.valid) return;
-    if (P.splits > 1) {
-      const long long at = (static_cast<long long>(split) * rows) +
-                           (static_cast<long long>(blockIdx.y) * P.tiles + tile) * (RW * 16) + r;
-      if (c0 == 0) P.part_ml[at] = make_float2(mm, ll);
-      float* to = P.part_o + at * D + c0;
+    // ---- merge the CTA's key groups, then write the rows (or their part, in
+    // the place of (CTA + sequence): one of the two grows from part to part)
+    auto put = [&](int r, const float* acc, float mm, float ll, int c0, int nc) {
+      // acc: nc channels from c0 of row r, unnormalised.
+      const CacheRow x = cache_row(P, r, h, s.len, count);
+      if (!x.valid) return;
+      if (!whole) {
+        const long long at = (static_cast<long long>(blockIdx.x + b) * P.c.H + h) * ROWS + r;
+        if (c0 == 0) P.part_ml[at] = make_float2(mm, ll);
+        float* to = P.part_o + at * D + c0;
 #pragma unroll
-      for (int c = 0; c < nc; c += 4)
-        *reinterpret_cast<float4*>(to + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
-      return;
-    }
-    const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-    char* to = P.o + b * P.ob + x.head * P.oh + x.n * P.on + 2 * c0;
-#pragma unroll
-    for (int c = 0; c < nc; c += 8)
-      *reinterpret_cast<uint4*>(to + 2 * c) =
-          make_uint4(pack_bf16x2(acc[c] * inv, acc[c + 1] * inv), pack_bf16x2(acc[c + 2] * inv, acc[c + 3] * inv),
-                     pack_bf16x2(acc[c + 4] * inv, acc[c + 5] * inv), pack_bf16x2(acc[c + 6] * inv, acc[c + 7] * inv));
-    if (c0 == 0 && P.lse != nullptr)
-      P.lse[(static_cast<long long>(b) * P.Hq + x.head) * P.N + x.n] = (mm + log2f(ll)) * 0.6931471805599453f;
-  };
-  if constexpr (KW == 1) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float acc[D / 4];
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        acc[j] = o[j][2 * i];
-        acc[NT + j] = o[j][2 * i + 1];
+        for (int c = 0; c < nc; c += 4)
+          *reinterpret_cast<float4*>(to + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+        return;
       }
-      put(rt * 16 + g + 8 * i, acc, ms[i], l[i], t * (D / 4), D / 4);
-    }
-  } else {
-    __syncthreads();                 // every group is done with the ring
+      const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+      char* to = P.o + b * P.ob + x.head * P.oh + x.n * P.on + 2 * c0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+      for (int c = 0; c < nc; c += 8)
+        *reinterpret_cast<uint4*>(to + 2 * c) =
+            make_uint4(pack_bf16x2(acc[c] * inv, acc[c + 1] * inv), pack_bf16x2(acc[c + 2] * inv, acc[c + 3] * inv),
+                       pack_bf16x2(acc[c + 4] * inv, acc[c + 5] * inv), pack_bf16x2(acc[c + 6] * inv, acc[c + 7] * inv));
+      if (c0 == 0 && P.lse != nullptr)
+        P.lse[(static_cast<long long>(b) * P.Hq + x.head) * P.N + x.n] = (mm + log2f(ll)) * 0.6931471805599453f;
+    };
+    if constexpr (KW == 1) {
 #pragma unroll
-      for (int j = 0; j < NT; j += 4) {
-        *reinterpret_cast<float4*>(&os[rt][kw][g + 8 * i][t * (D / 4) + j]) =
-            make_float4(o[j][2 * i], o[j + 1][2 * i], o[j + 2][2 * i], o[j + 3][2 * i]);
-        *reinterpret_cast<float4*>(&os[rt][kw][g + 8 * i][t * (D / 4) + NT + j]) =
-            make_float4(o[j][2 * i + 1], o[j + 1][2 * i + 1], o[j + 2][2 * i + 1], o[j + 3][2 * i + 1]);
+      for (int i = 0; i < 2; ++i) {
+        float acc[D / 4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          acc[j] = o[j][2 * i];
+          acc[NT + j] = o[j][2 * i + 1];
+        }
+        put(rt * 16 + g + 8 * i, acc, ms[i], l[i], t * (D / 4), D / 4);
       }
-      if (t == 0) mls[rt][kw][g + 8 * i] = make_float2(ms[i], l[i]);
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e < RW * 16 * (D / 8); e += kThreads) {
-      const int r = e / (D / 8), c0 = e % (D / 8) * 8;
-      const int w = r / 16, rr = r % 16;
-      float mm = -INFINITY, ll = 0.0f, acc[8] = {};
+    } else {
+      __syncthreads();                 // every group is done with the ring
 #pragma unroll
-      for (int k = 0; k < KW; ++k) mm = fmaxf(mm, mls[w][k][rr].x);
+      for (int i = 0; i < 2; ++i) {
 #pragma unroll
-      for (int k = 0; k < KW; ++k) {
-        const float2 p = mls[w][k][rr];
-        // A part that saw no key (its sum is 0) counts for nothing; one whose
-        // sum is NaN does.
-        if (p.y == 0.0f) continue;
-        const float f = p.x == -INFINITY ? 1.0f : ex2_ftz(p.x - mm);
-        ll = fmaf(p.y, f, ll);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) acc[c] = fmaf(os[w][k][rr][c0 + c], f, acc[c]);
+        for (int j = 0; j < NT; j += 4) {
+          *reinterpret_cast<float4*>(&os[rt][kw][g + 8 * i][t * (D / 4) + j]) =
+              make_float4(o[j][2 * i], o[j + 1][2 * i], o[j + 2][2 * i], o[j + 3][2 * i]);
+          *reinterpret_cast<float4*>(&os[rt][kw][g + 8 * i][t * (D / 4) + NT + j]) =
+              make_float4(o[j][2 * i + 1], o[j + 1][2 * i + 1], o[j + 2][2 * i + 1], o[j + 3][2 * i + 1]);
+        }
+        if (t == 0) mls[rt][kw][g + 8 * i] = make_float2(ms[i], l[i]);
       }
-      put(r, acc, mm, ll, c0, 8);
+      __syncthreads();
+      for (int e = threadIdx.x; e < RW * 16 * (D / 8); e += kThreads) {
+        const int r = e / (D / 8), c0 = e % (D / 8) * 8;
+        const int w = r / 16, rr = r % 16;
+        float mm = -INFINITY, ll = 0.0f, acc[8] = {};
+#pragma unroll
+        for (int k = 0; k < KW; ++k) mm = fmaxf(mm, mls[w][k][rr].x);
+#pragma unroll
+        for (int k = 0; k < KW; ++k) {
+          const float2 p = mls[w][k][rr];
+          // A part that saw no key (its sum is 0) counts for nothing; one whose
+          // sum is NaN does.
+          if (p.y == 0.0f) continue;
+          const float f = p.x == -INFINITY ? 1.0f : ex2_ftz(p.x - mm);
+          ll = fmaf(p.y, f, ll);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) acc[c] = fmaf(os[w][k][rr][c0 + c], f, acc[c]);
+        }
+        put(r, acc, mm, ll, c0, 8);
+      }
     }
+    // The ring and the fragments are the next sequence's.
+    fence_proxy_async_smem();
+    if (!__syncthreads_and(ok)) break;
   }
 }
 
-// Merges the splits of every row: a warp per row.
+// Merges the parts of the sequences that more than one CTA worked on: a warp
+// per row.
 template <int D>
-__global__ void __launch_bounds__(kThreads) cache_merge_kernel(const __grid_constant__ CacheAttnParams P, int rows_per_tile) {
+__global__ void __launch_bounds__(kThreads) cache_merge_kernel(const __grid_constant__ CacheAttnParams P, int rows, int slots) {
   const int lane = threadIdx.x % 32;
-  const int per = P.tiles * rows_per_tile;            // rows of a (sequence, key head)
-  const long long rows = static_cast<long long>(P.c.B) * P.c.H * per;
-  const long long at = static_cast<long long>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
-  if (at >= rows) return;
-  const int bh = static_cast<int>(at / per), r = static_cast<int>(at % per);
-  const int b = bh / P.c.H, h = bh % P.c.H;
+  const long long row = static_cast<long long>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (row >= static_cast<long long>(P.c.B) * P.c.H * rows) return;
+  const int r = static_cast<int>(row % rows), h = static_cast<int>(row / rows % P.c.H);
+  const int b = static_cast<int>(row / rows / P.c.H);
+  const long long w0 = P.plan[b], w1 = P.plan[b + 1], total = P.plan[P.c.B];
+  if (w0 == w1) return;
+  const long long ctas = run_ctas(total, slots);
+  // CTA x holds half pages [total x / ctas, total (x + 1) / ctas).
+  const int x0 = static_cast<int>(((w0 + 1) * ctas + total - 1) / total) - 1;
+  const int n = static_cast<int>((w1 * ctas + total - 1) / total) - x0;
+  if (n == 1) return;
   bool bad = false;                                   // reported by the attention
   const int count = P.counts == nullptr ? P.N : cache_count(__ldg(P.counts + b), P.N, &bad);
-  const int n = r / P.group, head = h * P.group + r % P.group;
-  if (n >= count) return;
-  // A split a lane (two past 32): its weight against the largest maximum, 0
-  // where it saw no key (its O is 0 too).
-  float2 p[2];
+  const int i_q = r / P.group, head = h * P.group + r % P.group;
+  if (i_q >= count) return;
+  const long long at = (static_cast<long long>(x0 + b) * P.c.H + h) * rows + r, step = static_cast<long long>(P.c.H) * rows;
+  // Four parts a lane (128 at most): a part's weight against the largest
+  // maximum, 0 where it saw no key (its O is 0 too).
+  float2 p[4];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-    p[i] = lane + 32 * i < P.splits ? P.part_ml[(lane + 32 * i) * rows + at] : make_float2(-INFINITY, 0.0f);
-  float mm = fmaxf(p[0].x, p[1].x);
+  for (int i = 0; i < 4; ++i)
+    p[i] = lane + 32 * i < n ? P.part_ml[at + (lane + 32 * i) * step] : make_float2(-INFINITY, 0.0f);
+  float mm = fmaxf(fmaxf(p[0].x, p[1].x), fmaxf(p[2].x, p[3].x));
 #pragma unroll
   for (int i = 16; i > 0; i /= 2) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, i));
-  float w[2], ll = 0.0f;
+  float w[4], ll = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < 4; ++i) {
     w[i] = p[i].y == 0.0f ? 0.0f : (p[i].x == -INFINITY ? 1.0f : ex2_ftz(p[i].x - mm));
     ll = fmaf(p[i].y, w[i], ll);
   }
@@ -623,55 +703,71 @@ __global__ void __launch_bounds__(kThreads) cache_merge_kernel(const __grid_cons
   constexpr int C = D / 32;
   float acc[C] = {};
   const float* from = P.part_o + at * D + lane * C;
-  // Eight splits' loads in flight.
-  for (int k0 = 0; k0 < P.splits; k0 += 8) {
+  // Eight parts' loads in flight.
+  for (int k0 = 0; k0 < n; k0 += 8) {
     float v[8][C];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int c = 0; c < C; ++c) v[i][c] = k0 + i < P.splits ? from[(k0 + i) * rows * D + c] : 0.0f;
+      for (int c = 0; c < C; ++c) v[i][c] = k0 + i < n ? from[(k0 + i) * step * D + c] : 0.0f;
+    const float wk = k0 < 32 ? w[0] : (k0 < 64 ? w[1] : (k0 < 96 ? w[2] : w[3]));
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float f = __shfl_sync(0xffffffffu, k0 < 32 ? w[0] : w[1], (k0 + i) % 32);
+      const float f = __shfl_sync(0xffffffffu, wk, (k0 + i) % 32);
 #pragma unroll
       for (int c = 0; c < C; ++c) acc[c] = fmaf(v[i][c], f, acc[c]);
     }
   }
   const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-  char* to = P.o + b * P.ob + head * P.oh + n * P.on + 2 * lane * C;
+  char* to = P.o + b * P.ob + head * P.oh + i_q * P.on + 2 * lane * C;
 #pragma unroll
   for (int c = 0; c < C; c += 2)
     *reinterpret_cast<uint32_t*>(to + 2 * c) = pack_bf16x2(acc[c] * inv, acc[c + 1] * inv);
   if (lane == 0 && P.lse != nullptr)
-    P.lse[(static_cast<long long>(b) * P.Hq + head) * P.N + n] = (mm + log2f(ll)) * 0.6931471805599453f;
+    P.lse[(static_cast<long long>(b) * P.Hq + head) * P.N + i_q] = (mm + log2f(ll)) * 0.6931471805599453f;
 }
 
-// Row warps, row tiles and splits of a call.
+// Row warps and CTAs per head of a call.
 struct Shape {
-  int rw, tiles, splits;
-  long long rows;              // padded rows of all (sequence, key head)
+  int rw, slots;
+  bool merge;                  // a sequence may be in more than one CTA
+  size_t part_o, part_ml, plan, total;
 };
 Shape shape_of(const CacheAttnArgs& a, int num_sms) {
   Shape s;
-  const long long rows = static_cast<long long>(a.Hq / a.cache.H) * a.N;
+  const int B = a.cache.B, H = a.cache.H;
+  const long long rows = static_cast<long long>(a.Hq / H) * a.N;
   s.rw = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
-  s.tiles = static_cast<int>((rows + s.rw * 16 - 1) / (s.rw * 16));
-  const long long bh = static_cast<long long>(a.cache.B) * a.cache.H;
-  s.rows = bh * s.tiles * s.rw * 16;
-  // One wave of CTAs, two to an SM, and two half pages to a key group at the
-  // least (of a full table).
-  const long long ctas = bh * s.tiles;
-  long long splits = 2ll * num_sms / ctas;
-  const long long most = (a.cache.blocks + 1ll) * 2 / (2 * (4 / s.rw));
-  if (splits > most) splits = most;
-  if (splits > 64) splits = 64;
-  s.splits = splits < 1 ? 1 : static_cast<int>(splits);
+  // One wave of two CTAs to an SM, each with eight half pages at the least (of
+  // a full table); 128 parts of a sequence at most, which is what a merging
+  // warp holds.  Past kScan sequences a CTA takes one of them each.
+  long long slots = 2ll * num_sms / H;
+  const long long most = (B * (2ll * a.cache.blocks + 2) + 7) / 8;
+  if (slots > most) slots = most;
+  if (slots > 128) slots = 128;
+  if (slots < 1) slots = 1;
+  s.merge = B <= kScan && slots > 1;
+  s.slots = B <= kScan ? static_cast<int>(slots) : B;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off += align256(bytes);
+    return o;
+  };
+  s.part_o = s.part_ml = s.plan = 0;
+  if (s.merge) {
+    const size_t parts = (static_cast<size_t>(s.slots) + B) * H * s.rw * 16;
+    s.part_o = take(parts * a.cache.d * sizeof(float));
+    s.part_ml = take(parts * sizeof(float2));
+    s.plan = take((static_cast<size_t>(B) + 1) * sizeof(long long));
+  }
+  s.total = off;
   return s;
 }
 
 template <int D, int RW>
 cudaError_t launch_rw(const Ctx& c, const CacheAttnParams& P, const Shape& s) {
-  const dim3 grid(static_cast<unsigned>(s.tiles) * s.splits, P.c.B * P.c.H);
+  const dim3 grid(s.slots, P.c.H);
   const cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D, RW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              Ring<D, RW>::kSmem);
   if (e != cudaSuccess) return e;
@@ -682,9 +778,19 @@ cudaError_t launch_rw(const Ctx& c, const CacheAttnParams& P, const Shape& s) {
 template <int D>
 cudaError_t launch_d(const Ctx& c, const CacheAttnParams& P, const Shape& s) {
   const cudaError_t e = s.rw == 1 ? launch_rw<D, 1>(c, P, s) : (s.rw == 2 ? launch_rw<D, 2>(c, P, s) : launch_rw<D, 4>(c, P, s));
-  if (e != cudaSuccess || s.splits == 1) return e;
-  cache_merge_kernel<D><<<static_cast<unsigned>((s.rows + 3) / 4), kThreads, 0, c.stream>>>(P, s.rw * 16);
-  return cudaGetLastError();
+  if (e != cudaSuccess || !s.merge) return e;
+  const long long rows = static_cast<long long>(P.c.B) * P.c.H * s.rw * 16;
+  // Launched while the attention runs; it waits for its end before it reads.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + kThreads / 32 - 1) / (kThreads / 32)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = c.stream;
+  cudaLaunchAttribute early = {};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_merge_kernel<D>, P, s.rw * 16, s.slots);
 }
 
 }  // namespace
@@ -696,10 +802,7 @@ static bool many_rows(const CacheAttnArgs& a) {
 
 size_t cache_attn_ws_bytes(const CacheAttnArgs& a, int num_sms) {
   if (many_rows(a)) return cache_attn_tc_ws_bytes(a, num_sms);
-  const Shape s = shape_of(a, num_sms);
-  if (s.splits == 1) return 0;
-  const size_t rows = static_cast<size_t>(s.rows) * s.splits;
-  return align256(rows * a.cache.d * sizeof(float)) + align256(rows * sizeof(float2));
+  return shape_of(a, num_sms).total;
 }
 
 cudaError_t launch_cache_attn(const Ctx& c, const CacheAttnArgs& a) {
@@ -722,14 +825,15 @@ cudaError_t launch_cache_attn(const Ctx& c, const CacheAttnArgs& a) {
   P.wait_ns = c.wait_ns;
   P.part_o = nullptr;
   P.part_ml = nullptr;
+  P.plan = nullptr;
   if (many_rows(a)) return launch_cache_attn_tc(c, a, P);
   const Shape s = shape_of(a, c.num_sms);
-  P.tiles = s.tiles;
-  P.splits = s.splits;
-  if (s.splits > 1) {
-    const size_t rows = static_cast<size_t>(s.rows) * s.splits;
-    P.part_o = static_cast<float*>(a.workspace);
-    P.part_ml = reinterpret_cast<float2*>(static_cast<char*>(a.workspace) + align256(rows * a.cache.d * sizeof(float)));
+  P.tiles = 1;
+  if (s.merge) {
+    char* ws = static_cast<char*>(a.workspace);
+    P.part_o = reinterpret_cast<float*>(ws + s.part_o);
+    P.part_ml = reinterpret_cast<float2*>(ws + s.part_ml);
+    P.plan = reinterpret_cast<long long*>(ws + s.plan);
   }
   return a.cache.d == 128 ? launch_d<128>(c, P, s) : launch_d<64>(c, P, s);
 }

@@ -22,9 +22,9 @@ struct CacheAttnParams {
   int frame, window;
   float scale_log2;                   // softmax scale * log2(e)
   int tiles;                          // row tiles of one (sequence, key head)
-  int splits;
-  float* part_o;                      // [splits][B * H * tiles * rows][d]
-  float2* part_ml;                    // [splits][B * H * tiles * rows]
+  float* part_o;                      // unnormalised parts of rows, for the merging launch
+  float2* part_ml;                    // their maxima and sums
+  long long* plan;                    // [B + 1], prefix sums of the sequences' work
   unsigned* err;
   unsigned long long wait_ns;
 };

@@ -1069,7 +1069,6 @@ cudaError_t launch_cache_attn_tc(const Ctx& c, const CacheAttnArgs& a, CacheAttn
   char* ws = static_cast<char*>(a.workspace);
   TcParams T;
   P.tiles = L.tiles;
-  P.splits = 0;
   P.part_o = reinterpret_cast<float*>(ws + L.part_o);
   P.part_ml = reinterpret_cast<float2*>(ws + L.part_ml);
   T.a = P;
