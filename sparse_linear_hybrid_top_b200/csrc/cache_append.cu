@@ -12,8 +12,9 @@
 // HBM-bound.  CTA (block of the sequence, group of heads, sequence): 256
 // threads, four to a row; a thread holds its quarter of the row's keys and
 // values in registers, so the block is read once, its two maxima are taken
-// over registers, and the codes are written from them.  The cosines and sines
-// of the row are formed once and serve every head of the group.
+// over registers, and the codes are written from them.  The next head's rows
+// travel while one is encoded.  The cosines and sines of the block's rows are
+// formed once, in shared memory, and serve every head of the group.
 #include <cuda_fp8.h>
 
 #include "cache_index.h"
@@ -73,9 +74,12 @@ __device__ __forceinline__ uint2 to_codes(uint4 x, float inverse) {
 }
 
 template <int D, bool HALVES>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams P) {
+__global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_constant__ AppendParams P) {
   constexpr int CH = D / 32;                     // 16-byte chunks of a row per thread
   __shared__ double turns[D / 2];
+  // Cosines and sines of the rows' pairs; a row's pad keeps its neighbour's in
+  // other banks.
+  __shared__ __align__(16) float2 cs[kCacheBlock][D / 2 + 2];
   __shared__ uint32_t top[2][2][kThreads / 32];  // [parity][K or V][warp]
   const int b = blockIdx.z;
   bool bad = false;
@@ -105,58 +109,84 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
       return;
     }
   }
-  float2 cs[D / 8];
   if (P.rotate) {
     for (int m = threadIdx.x; m < D / 2; m += kThreads) turns[m] = P.rates.turns[m];
     __syncthreads();
     if (fresh) {
+      // Each thread the pairs that it uses itself.
       const int3 pos = rope_position(P.where, b, i, s.len + i);
-#pragma unroll
+#pragma unroll 4
       for (int x = 0; x < D / 8; ++x) {
         // Adjacent: chunk quarter + 4 (x / 4) holds pairs 4 chunk ..; halves:
         // the eight pairs of chunk quarter + 4 (x / 8) and the one D/2 on.
         const int m = HALVES ? 8 * (quarter + 4 * (x / 8)) + x % 8 : 4 * (quarter + 4 * (x / 4)) + x % 4;
         const int at = m < P.rates.first1 ? pos.x : (m < P.rates.first2 ? pos.y : pos.z);
-        cs[x] = rope_cos_sin(turns[m], at);
+        cs[row][m] = rope_cos_sin(turns[m], at);
       }
     }
   }
   const int h0 = blockIdx.y * P.heads_per_cta, h1 = min(P.c.H, h0 + P.heads_per_cta);
-  for (int h = h0; h < h1; ++h) {
-    uint4 k[CH], v[CH];
+  // A row that is neither new nor part of a closing block is not touched.
+  const bool has = fresh || closes;
+  auto load = [&](int h, uint4 (&k)[CH], uint4 (&v)[CH]) {
     const long long old = (((static_cast<long long>(b) * 2 + s.slot) * P.c.H + h) * kCacheBlock + row) * D * 2;
     const char* kp = fresh ? P.k + b * P.kb + h * P.kh + i * P.kn : reinterpret_cast<const char*>(P.c.k_tail) + old;
     const char* vp = fresh ? P.v + b * P.vb + h * P.vh + i * P.vn : reinterpret_cast<const char*>(P.c.v_tail) + old;
-    // A row that is neither new nor part of a closing block is not touched.
-    const bool has = fresh || closes;
 #pragma unroll
     for (int x = 0; x < CH; ++x) {
       k[x] = has ? __ldcs(reinterpret_cast<const uint4*>(kp) + quarter + 4 * x) : make_uint4(0, 0, 0, 0);
       v[x] = has ? __ldcs(reinterpret_cast<const uint4*>(vp) + quarter + 4 * x) : make_uint4(0, 0, 0, 0);
     }
+  };
+  uint4 k_next[CH], v_next[CH];
+  load(h0, k_next, v_next);
+  for (int h = h0; h < h1; ++h) {
+    uint4 k[CH], v[CH];
+#pragma unroll
+    for (int x = 0; x < CH; ++x) {
+      k[x] = k_next[x];
+      v[x] = v_next[x];
+    }
+    if (h + 1 < h1) load(h + 1, k_next, v_next);
     if (P.rotate && fresh) {
+      // Four cosines and sines at an address: two 16-byte reads.
+      auto pairs = [&](int m, float2 (&c)[4]) {
+        const float4 lo = *reinterpret_cast<const float4*>(&cs[row][m]);
+        const float4 hi = *reinterpret_cast<const float4*>(&cs[row][m + 2]);
+        c[0] = make_float2(lo.x, lo.y);
+        c[1] = make_float2(lo.z, lo.w);
+        c[2] = make_float2(hi.x, hi.y);
+        c[3] = make_float2(hi.z, hi.w);
+      };
       if (HALVES) {
 #pragma unroll
         for (int x = 0; x < CH / 2; ++x) {
           uint32_t* u = &k[x].x;
           uint32_t* w = &k[x + CH / 2].x;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 a = unpack_bf16x2(u[e]), c = unpack_bf16x2(w[e]);
-            const float2 lo = rope_turn(a.x, c.x, cs[8 * x + 2 * e]);
-            const float2 hi = rope_turn(a.y, c.y, cs[8 * x + 2 * e + 1]);
-            u[e] = pack_bf16x2(lo.x, hi.x);
-            w[e] = pack_bf16x2(lo.y, hi.y);
+          for (int y = 0; y < 2; ++y) {
+            float2 c[4];
+            pairs(8 * (quarter + 4 * x) + 4 * y, c);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float2 p = unpack_bf16x2(u[2 * y + e]), q = unpack_bf16x2(w[2 * y + e]);
+              const float2 lo = rope_turn(p.x, q.x, c[2 * e]);
+              const float2 hi = rope_turn(p.y, q.y, c[2 * e + 1]);
+              u[2 * y + e] = pack_bf16x2(lo.x, hi.x);
+              w[2 * y + e] = pack_bf16x2(lo.y, hi.y);
+            }
           }
         }
       } else {
 #pragma unroll
         for (int x = 0; x < CH; ++x) {
           uint32_t* u = &k[x].x;
+          float2 c[4];
+          pairs(4 * (quarter + 4 * x), c);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 a = unpack_bf16x2(u[e]);
-            const float2 r = rope_turn(a.x, a.y, cs[4 * x + e]);
+            const float2 p = unpack_bf16x2(u[e]);
+            const float2 r = rope_turn(p.x, p.y, c[e]);
             u[e] = pack_bf16x2(r.x, r.y);
           }
         }
@@ -243,11 +273,15 @@ cudaError_t launch_cache_append(const Ctx& c, const CacheAppendArgs& a) {
   if (a.rotate) P.rates = rope_rates(a.split, a.base);
   else P.rates = RopeRates{};
   P.err = c.err;
-  // Blocks that N tokens can touch.  Heads share a CTA (and its cosines)
-  // where the blocks alone give each SM four CTAs.
+  // Blocks that N tokens can touch.  Heads share a CTA (and its cosines) as
+  // far as the CTAs still fill two places on every SM, and eight at most, so
+  // that CTAs behind a padded batch's counts, which end at once, do not leave
+  // others a second turn (4 x 40 heads x 3600 padded tokens: 74 us with four
+  // heads to a CTA, 66 with eight, 72 with twelve).
   const int span = (a.N + kCacheBlock - 1) / kCacheBlock + 1;
   const long long units = static_cast<long long>(span) * a.cache.B * a.cache.H;
-  long long per = units / (4ll * c.num_sms);
+  long long per = units / (2ll * c.num_sms);
+  if (per > 8) per = 8;
   if (per < 1) per = 1;
   if (per > a.cache.H) per = a.cache.H;
   P.heads_per_cta = static_cast<int>(per);
