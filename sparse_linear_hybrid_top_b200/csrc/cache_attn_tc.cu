@@ -61,7 +61,7 @@ struct CT {
   static constexpr int kStages = 4;                     // operand tiles
   static constexpr int kRaw = 128 * D;                  // codes of an operand tile
   static constexpr int kRaws = D == 128 ? 2 : 4;
-  static constexpr int kBarBytes = 256;
+  static constexpr int kBarBytes = 320;
   static constexpr int kScaleBytes = 8 * 16 + 8 * 8;    // scales of eight tiles (K, K, V, V), eight parts' (tiles, slots)
   static constexpr int kSegBytes = 8 * 64;              // the softmax warps' current parts
   static constexpr int kUsed = (2 + kStages) * kOperand + kRaws * kRaw + kBarBytes + kScaleBytes + kSegBytes;
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
   unsigned char* ring = qbuf + 2 * C::kOperand;             // [NS][d-slab][128 rows]
   unsigned char* raws = ring + NS * C::kOperand;            // [NR][128 keys][d codes]
   uint64_t* bars = reinterpret_cast<uint64_t*>(raws + NR * C::kRaw);
-  // full[NS] empty[NS] raw_full[NR] raw_empty[NR] q_full[2] q_free[2] s_full[2] p_full[2] o_done[2] drain
+  // full[NS] empty[NS] raw_full[NR] raw_empty[NR] q_full[2] q_free[2] s_full[2] p_half[2] p_full[2] o_done[2] drain
   auto bar = [&](int i) { return smem_u32(bars + i); };
   auto full = [&](int i) { return bar(i); };
   auto empty = [&](int i) { return bar(NS + i); };
@@ -340,14 +340,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
   auto q_full = [&](int i) { return bar(B0 + i); };
   auto q_free = [&](int i) { return bar(B0 + 2 + i); };
   auto s_full = [&](int i) { return bar(B0 + 4 + i); };
-  auto p_full = [&](int i) { return bar(B0 + 6 + i); };
-  auto o_done = [&](int i) { return bar(B0 + 8 + i); };
-  const uint32_t drain = bar(B0 + 10);
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + B0 + 11);
+  auto p_half = [&](int i) { return bar(B0 + 6 + i); };
+  auto p_full = [&](int i) { return bar(B0 + 8 + i); };
+  auto o_done = [&](int i) { return bar(B0 + 10 + i); };
+  const uint32_t drain = bar(B0 + 12);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + B0 + 13);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   // odd_seg[i % 8] = i + 1: part i's open block holds a value that is not finite.
   volatile int* odd_seg = abort_flag + 1;
-  static_assert((B0 + 11) * 8 + 4 + 4 + 32 <= C::kBarBytes, "barrier region");
+  static_assert((B0 + 13) * 8 + 4 + 4 + 32 <= C::kBarBytes, "barrier region");
   // Scales of tile i's two blocks in entry i % 8: of the keys (0: no page, its
   // keys do not count), then of the values.  Warp 13 writes them with the bulk
   // copy of the tile's keys: kRaws operand tiles before these are converted,
@@ -376,6 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
       mbar_init(q_full(i), 4);    // the slot's four softmax warps
       mbar_init(q_free(i), 1);
       mbar_init(s_full(i), 1);
+      mbar_init(p_half(i), 4);
       mbar_init(p_full(i), 4);
       mbar_init(o_done(i), 1);
     }
@@ -444,20 +446,27 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
           const uint64_t vd = sdesc_sw128(ring_base + st * C::kOperand, C::kRowSlab, 1024);
           const int kst = st + 1 == NS ? 0 : st + 1;
           const uint32_t kph = st + 1 == NS ? ph ^ 1u : ph;
+          // Both are there before the first P, as a rule.
+          ok = wait_stage() && (t + 1 == n || mbar_wait_poll(full(kst), kph, wait_ns, abort_flag));
           for (int slot = 0; slot < slots && ok; ++slot) {
-            ok = mbar_wait_spin(p_full(slot), pn[slot]++ & 1u, wait_ns, abort_flag) && (slot > 0 || wait_stage());
+            const uint32_t sa = tmem + C::s_col(slot) + 64, oa = tmem + C::o_col(slot);
+            auto pv = [&](int ks, uint32_t acc) {   // 16 keys
+              mma_ts(oa, sa + ks * 8, vd + static_cast<uint64_t>((ks * 2048) >> 4), idesc_pv, acc);
+            };
+            // The tile's second half comes first.
+            ok = mbar_wait_spin(p_half(slot), pn[slot] & 1u, wait_ns, abort_flag);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t sa = tmem + C::s_col(slot), oa = tmem + C::o_col(slot);
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks)      // 16 keys each
-              mma_ts(oa, sa + 64 + ks * 8, vd + static_cast<uint64_t>((ks * 2048) >> 4), idesc_pv,
-                     ks > 0 ? 1u : (t > 0 ? 1u : 0u));
+            for (int ks = 4; ks < 8; ++ks) pv(ks, ks > 4 || t > 0 ? 1u : 0u);
+            ok = mbar_wait_spin(p_full(slot), pn[slot]++ & 1u, wait_ns, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) pv(ks, 1u);
             if (t + 1 == n) {
               mma_commit(o_done(slot));
             } else {
-              if (slot == 0 && !mbar_wait_poll(full(kst), kph, wait_ns, abort_flag)) { ok = false; break; }
-              tc_fence_after();
               issue_qk(slot, kst);               // over this slot's P: behind its PV in issue order
               if (t + 2 == n) mma_commit(q_free(slot));
             }
@@ -762,6 +771,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
           }
           ++sn;
           tc_fence_after();
+          uint32_t sv[64], sw[64];
+          tmem_ld64_async(sbuf, sv);
           const float4 sc = scales[(tile_no + t) % 8];
           const int kb = (j0 + t) * kTile;
           // Halves outside some row's range: scores there become -inf, in
@@ -786,11 +797,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
               tmem_st32(sbuf + c0, s32);
             }
             tmem_st_wait();
+            tmem_ld64_async(sbuf, sv);
           }
           // Pass 1: the row's maxima.  The second half's scores stay in
           // registers; the first half's are read again in pass 2.
-          uint32_t sv[64], sw[64];
-          tmem_ld64_async(sbuf, sv);
           tmem_arrived();
           tmem_ld64_async(sbuf + 64, sw);               // travels while the first half is reduced
           pin64(sv);
@@ -807,6 +817,18 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
           if (pm > mt + 8.0f) {
             f = mt == -INFINITY ? 1.0f : ex2_ftz(mt - pm);
             mt = pm;
+          }
+          // The slot's previous PV was issued before this tile's QK, whose
+          // commit has arrived: O may be rescaled.
+          if (t > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 32) {
+              uint32_t o32[32];
+              tmem_ld32(obuf + c0, o32);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o32[e] = __float_as_uint(__uint_as_float(o32[e]) * f);
+              tmem_st32(obuf + c0, o32);
+            }
           }
           const float top = fmaxf(ms, fmaxf(s0, s1));
           if (top > ms) {
@@ -832,8 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
           if (far0) far_sum(0, c20);
           // Pass 2: 32 scores as 16 pairs of P, at columns 64 and up of S (the
           // second half's scores have left them).
-          uint64_t sum0 = 0, sum1 = 0;
-          auto weights = [&](const uint32_t* v, uint64_t c22, uint64_t off, uint32_t to) {
+          auto weights = [&](const uint32_t* v, uint64_t c22, uint64_t off, uint32_t to, uint64_t& sum0, uint64_t& sum1) {
             uint32_t pk[16];
 #pragma unroll
             for (int c = 0; c < 32; c += 4) {
@@ -851,47 +872,41 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
             }
             tmem_st16(to, pk);
           };
-          auto take_sum = [&](bool far, float ev) {
-            float u0, u1;
-            unpack2(add2(sum0, sum1), u0, u1);
-            if (!far) add = fmaf(u0 + u1, ex2_ftz(ns - nm - ev), add);
-            sum0 = sum1 = 0;
+          // P of a half is in TMEM: its PV may start.
+          auto hand_over = [&](uint32_t to) {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(to);
           };
+          uint64_t sum1a = 0, sum1b = 0, sum0a = 0, sum0b = 0;
           {
             const uint64_t c22 = pack2(c21, c21), off = pack2(nm + ev1, nm + ev1);
+            weights(sw, c22, off, sbuf + 96, sum1a, sum1b);
             tmem_ld32_async(sbuf, sv);
-            weights(sw, c22, off, sbuf + 96);
-            weights(sw + 32, c22, off, sbuf + 112);
-            take_sum(far1, ev1);
+            weights(sw + 32, c22, off, sbuf + 112, sum1a, sum1b);
+            hand_over(p_half(slot));
           }
           {
             const uint64_t c22 = pack2(c20, c20), off = pack2(nm + ev0, nm + ev0);
             tmem_arrived();
             pin32(sv);
             tmem_ld32_async(sbuf + 32, sv + 32);
-            weights(sv, c22, off, sbuf + 64);
+            weights(sv, c22, off, sbuf + 64, sum0a, sum0b);
             tmem_arrived();
             pin32(sv + 32);
-            weights(sv + 32, c22, off, sbuf + 80);
-            take_sum(far0, ev0);
+            weights(sv + 32, c22, off, sbuf + 80, sum0a, sum0b);
+            hand_over(p_full(slot));
           }
+          // The sums are not on the way to the next product.
+          auto take_sum = [&](uint64_t a, uint64_t b, bool far, float ev) {
+            float u0, u1;
+            unpack2(add2(a, b), u0, u1);
+            if (!far) add = fmaf(u0 + u1, ex2_ftz(ns - nm - ev), add);
+          };
+          take_sum(sum1a, sum1b, far1, ev1);
+          take_sum(sum0a, sum0b, far0, ev0);
           l += add;
-          // The slot's previous PV was issued before this tile's QK, whose
-          // commit has arrived: O may be rescaled.
-          if (t > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
-#pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 32) {
-              uint32_t o32[32];
-              tmem_ld32(obuf + c0, o32);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o32[e] = __float_as_uint(__uint_as_float(o32[e]) * f);
-              tmem_st32(obuf + c0, o32);
-            }
-          }
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(p_full(slot));
         }
         if (!ok) break;
         // Every QK of the part has run: the next part's Q, while its last PV does.
