@@ -24,10 +24,10 @@
 //                      their slot's rows of Q
 //   warps 8..11        codes -> fp16: from a ring of bulk-copied code tiles
 //                      to swizzled operand tiles
-//   warp 12            TMEM allocation and the single MMA-issuing thread
+//   warps 12, 14       the MMA issuers of slots 0 and 1 (12 holds the TMEM)
 //   warp 13            bulk copies of code tiles; it also passes the blocks'
 //                      scales to the softmax warps
-//   warps 14, 15       nothing: they fill the warpgroup that gives registers
+//   warp 15            nothing: it fills the warpgroup that gives registers
 // While the tensor pipe runs one slot's PV(t) and QK(t+1), the other slot's
 // softmax runs.  P overwrites S in TMEM.
 //
@@ -61,7 +61,7 @@ struct CT {
   static constexpr int kStages = 4;                     // operand tiles
   static constexpr int kRaw = 128 * D;                  // codes of an operand tile
   static constexpr int kRaws = D == 128 ? 2 : 4;
-  static constexpr int kBarBytes = 320;
+  static constexpr int kBarBytes = 384;
   static constexpr int kScaleBytes = 8 * 16 + 8 * 8;    // scales of eight tiles (K, K, V, V), eight parts' (tiles, slots)
   static constexpr int kSegBytes = 8 * 64;              // the softmax warps' current parts
   static constexpr int kUsed = (2 + kStages) * kOperand + kRaws * kRaw + kBarBytes + kScaleBytes + kSegBytes;
@@ -263,31 +263,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// Asynchronous TMEM load of 64 columns; the registers hold it after tmem_arrived.
-__device__ __forceinline__ void tmem_ld64_async(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
-      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
-      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
-      : SALAD_R8(r, 0), SALAD_R8(r, 8), SALAD_R8(r, 16), SALAD_R8(r, 24), SALAD_R8(r, 32),
-        SALAD_R8(r, 40), SALAD_R8(r, 48), SALAD_R8(r, 56)
-      : "r"(taddr)
-      : "memory");
-}
-#define SALAD_RW8(a, o) "+r"(a[o + 0]), "+r"(a[o + 1]), "+r"(a[o + 2]), "+r"(a[o + 3]), \
-                        "+r"(a[o + 4]), "+r"(a[o + 5]), "+r"(a[o + 6]), "+r"(a[o + 7])
-// Waits for every load of this thread.
-__device__ __forceinline__ void tmem_arrived() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-// Keeps uses of r behind the wait before it.
-__device__ __forceinline__ void pin64(uint32_t* r) {
-  asm volatile("" : SALAD_RW8(r, 0), SALAD_RW8(r, 8));
-  asm volatile("" : SALAD_RW8(r, 16), SALAD_RW8(r, 24));
-  asm volatile("" : SALAD_RW8(r, 32), SALAD_RW8(r, 40));
-  asm volatile("" : SALAD_RW8(r, 48), SALAD_RW8(r, 56));
-}
-
+// Asynchronous TMEM load of 32 columns; the registers hold it after tmem_arrived.
 __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -297,9 +273,42 @@ __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t* r) {
       : "r"(taddr)
       : "memory");
 }
+#define SALAD_RW8(a, o) "+r"(a[o + 0]), "+r"(a[o + 1]), "+r"(a[o + 2]), "+r"(a[o + 3]), \
+                        "+r"(a[o + 4]), "+r"(a[o + 5]), "+r"(a[o + 6]), "+r"(a[o + 7])
+// Waits for every load of this thread.
+__device__ __forceinline__ void tmem_arrived() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Keeps uses of r behind the wait before it.
 __device__ __forceinline__ void pin32(uint32_t* r) {
   asm volatile("" : SALAD_RW8(r, 0), SALAD_RW8(r, 8));
   asm volatile("" : SALAD_RW8(r, 16), SALAD_RW8(r, 24));
+}
+
+// MMAs and commits by one elected thread of a converged warp.  (The same
+// thread each time: commits track that thread's operations.)
+__device__ __forceinline__ void mma_ss_elected(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_elected(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void commit_elected(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar)
+      : "memory");
 }
 
 // The power of two that brings magnitudes up to bf16 bits `top` (finite) to
@@ -330,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
   unsigned char* ring = qbuf + 2 * C::kOperand;             // [NS][d-slab][128 rows]
   unsigned char* raws = ring + NS * C::kOperand;            // [NR][128 keys][d codes]
   uint64_t* bars = reinterpret_cast<uint64_t*>(raws + NR * C::kRaw);
-  // full[NS] empty[NS] raw_full[NR] raw_empty[NR] q_full[2] q_free[2] s_full[2] p_half[2] p_full[2] o_done[2] drain
+  // full[NS] empty[NS] raw_full[NR] raw_empty[NR] q_full[2] q_free[2] s_full[2] p_half[2] p_full[2] o_done[2] drain[2] turn[8]
   auto bar = [&](int i) { return smem_u32(bars + i); };
   auto full = [&](int i) { return bar(i); };
   auto empty = [&](int i) { return bar(NS + i); };
@@ -343,12 +352,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
   auto p_half = [&](int i) { return bar(B0 + 6 + i); };
   auto p_full = [&](int i) { return bar(B0 + 8 + i); };
   auto o_done = [&](int i) { return bar(B0 + 10 + i); };
-  const uint32_t drain = bar(B0 + 12);
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + B0 + 13);
+  auto drain = [&](int i) { return bar(B0 + 12 + i); };
+  auto turn = [&](int w) { return bar(B0 + 14 + w); };      // of softmax warp w
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + B0 + 22);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   // odd_seg[i % 8] = i + 1: part i's open block holds a value that is not finite.
   volatile int* odd_seg = abort_flag + 1;
-  static_assert((B0 + 13) * 8 + 4 + 4 + 32 <= C::kBarBytes, "barrier region");
+  static_assert((B0 + 22) * 8 + 4 + 4 + 32 <= C::kBarBytes, "barrier region");
   // Scales of tile i's two blocks in entry i % 8: of the keys (0: no page, its
   // keys do not count), then of the values.  Warp 13 writes them with the bulk
   // copy of the tile's keys: kRaws operand tiles before these are converted,
@@ -367,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(full(i), 4);      // the four converting warps
-      mbar_init(empty(i), 1);
+      mbar_init(empty(i), 2);     // the two issuers
     }
     for (int i = 0; i < NR; ++i) {
       mbar_init(raw_full(i), 1);
@@ -381,7 +391,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
       mbar_init(p_full(i), 4);
       mbar_init(o_done(i), 1);
     }
-    mbar_init(drain, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(drain(i), 1);
+    for (int i = 0; i < 8; ++i) mbar_init(turn(i), 1);
     *abort_flag = 0;
     for (int i = 0; i < 8; ++i) odd_seg[i] = 0;
     fence_mbar_init();
@@ -398,88 +409,99 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
   // Every warp of every warpgroup passes one of these three.
   if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLast));
-    if (warp == 12 && lane == 0) {
-      // ===================================================== MMA issuer
+    if (warp == 12 || warp == 14) {
+      // ============================================ MMA issuer of a slot
+      // An issuer a slot: every barrier that a warp looks at costs it some 300
+      // cycles beside the converting warps' traffic, and one warp with both
+      // slots' six a tile was the slowest of all.  The whole warp walks through
+      // the tiles, so that descriptors stay in uniform registers; one elected
+      // thread issues.
+      const int slot = warp == 12 ? 0 : 1;
       constexpr uint32_t idesc_qk = idesc_f16(128, 128, false, false);
       constexpr uint32_t idesc_pv = idesc_f16(128, D, false, true);
       const uint32_t ring_base = smem_u32(ring);
-      const uint64_t qd[2] = {sdesc_sw128(smem_u32(qbuf), 16, 1024),
-                              sdesc_sw128(smem_u32(qbuf) + C::kOperand, 16, 1024)};
+      const uint64_t qd = sdesc_sw128(smem_u32(qbuf) + slot * C::kOperand, 16, 1024);
+      const uint64_t kd0 = sdesc_sw128(ring_base, 16, 1024);
+      const uint64_t vd0 = sdesc_sw128(ring_base, C::kRowSlab, 1024);
+      constexpr uint64_t kStageStep = C::kOperand >> 4;
+      const uint32_t s_at = tmem + C::s_col(slot), p_at = s_at, o_at = tmem + C::o_col(slot);
       // Operand stage and phase of the next K or V, in the order K0 V0 K1 V1 ...
       int st = 0;
       uint32_t ph = 0;
-      uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};
+      uint32_t qn = 0, pn = 0;              // phases of q_full, and of p_half and p_full
       bool ok = true;
-      auto wait_stage = [&]() -> bool { return mbar_wait_poll(full(st), ph, wait_ns, abort_flag); };
-      auto next_stage = [&]() {
-        mma_commit(empty(st));
+      auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait_spin(bar, parity, wait_ns, abort_flag));
+      };
+      // This slot is done with the stage (once the MMAs so far are).
+      auto next_stage = [&](bool mine) {
+        if (mine) commit_elected(empty(st));
+        else if (lane == 0) mbar_arrive(empty(st));
         if (++st == NS) {
           st = 0;
           ph ^= 1u;
         }
       };
-      auto issue_qk = [&](int slot, int stage) {
-        const uint64_t kd = sdesc_sw128(ring_base + stage * C::kOperand, 16, 1024);
+      auto issue_qk = [&](int stage) {
+        const uint64_t kd = kd0 + static_cast<uint64_t>(stage) * kStageStep;
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint64_t off = static_cast<uint64_t>(((ks / 4) * C::kRowSlab + (ks % 4) * 32) >> 4);
-          mma_ss(tmem + C::s_col(slot), qd[slot] + off, kd + off, idesc_qk, ks > 0 ? 1u : 0u);
+          mma_ss_elected(s_at, qd + off, kd + off, idesc_qk, ks > 0 ? 1u : 0u);
         }
-        mma_commit(s_full(slot));
+        commit_elected(s_full(slot));
       };
       int left = static_cast<int>(w1 - w0);
-      for (int part_no = 0; left > 0 && ok; ++part_no) {
-        if (!wait_stage()) { ok = false; break; }
+      for (int part_no = 0; left > 0; ++part_no) {
+        if (!(ok = wait(full(st), ph))) break;
         const int2 info = part_info[part_no % 8];
-        const int n = info.x, slots = info.y;
-        for (int slot = 0; slot < slots && ok; ++slot) {
-          ok = mbar_wait_poll(q_full(slot), qn[slot]++ & 1u, wait_ns, abort_flag);
-          if (!ok) break;
+        const int n = info.x;
+        const bool mine = slot < info.y;
+        if (mine) {
+          if (!(ok = wait(q_full(slot), qn))) break;
+          qn ^= 1u;
           tc_fence_after();
-          issue_qk(slot, st);
-          if (n == 1) mma_commit(q_free(slot));
+          issue_qk(st);
+          if (n == 1) commit_elected(q_free(slot));
         }
-        if (!ok) break;
-        next_stage();
-        for (int t = 0; t < n && ok; ++t) {
-          // V(t) in this stage, K(t + 1) in the next.
-          const uint64_t vd = sdesc_sw128(ring_base + st * C::kOperand, C::kRowSlab, 1024);
+        next_stage(mine);
+        for (int t = 0; t < n; ++t) {
+          // V(t) in this stage, K(t + 1) in the next; both are there before P,
+          // as a rule.
           const int kst = st + 1 == NS ? 0 : st + 1;
           const uint32_t kph = st + 1 == NS ? ph ^ 1u : ph;
-          // Both are there before the first P, as a rule.
-          ok = wait_stage() && (t + 1 == n || mbar_wait_poll(full(kst), kph, wait_ns, abort_flag));
-          for (int slot = 0; slot < slots && ok; ++slot) {
-            const uint32_t sa = tmem + C::s_col(slot) + 64, oa = tmem + C::o_col(slot);
+          const uint64_t vd = vd0 + static_cast<uint64_t>(st) * kStageStep;
+          if (!(ok = wait(full(st), ph) && (t + 1 == n || wait(full(kst), kph)))) break;
+          if (mine) {
             auto pv = [&](int ks, uint32_t acc) {   // 16 keys
-              mma_ts(oa, sa + ks * 8, vd + static_cast<uint64_t>((ks * 2048) >> 4), idesc_pv, acc);
+              mma_ts_elected(o_at, p_at + ks * 8, vd + static_cast<uint64_t>((ks * 2048) >> 4), idesc_pv, acc);
             };
-            // The tile's second half comes first.
-            ok = mbar_wait_spin(p_half(slot), pn[slot] & 1u, wait_ns, abort_flag);
-            if (!ok) break;
+            // Half a tile's P at a time.
+            if (!(ok = wait(p_half(slot), pn))) break;
             tc_fence_after();
 #pragma unroll
-            for (int ks = 4; ks < 8; ++ks) pv(ks, ks > 4 || t > 0 ? 1u : 0u);
-            ok = mbar_wait_spin(p_full(slot), pn[slot]++ & 1u, wait_ns, abort_flag);
-            if (!ok) break;
+            for (int ks = 0; ks < 4; ++ks) pv(ks, ks > 0 || t > 0 ? 1u : 0u);
+            if (!(ok = wait(p_full(slot), pn))) break;
+            pn ^= 1u;
             tc_fence_after();
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) pv(ks, 1u);
+            for (int ks = 4; ks < 8; ++ks) pv(ks, 1u);
             if (t + 1 == n) {
-              mma_commit(o_done(slot));
+              commit_elected(o_done(slot));
             } else {
-              issue_qk(slot, kst);               // over this slot's P: behind its PV in issue order
-              if (t + 2 == n) mma_commit(q_free(slot));
+              issue_qk(kst);                        // over this tile's P: behind its PV in issue order
+              if (t + 2 == n) commit_elected(q_free(slot));
             }
           }
-          if (!ok) break;
-          next_stage();
-          if (t + 1 < n) next_stage();
+          next_stage(mine);
+          if (t + 1 < n) next_stage(mine);
         }
+        if (!ok) break;
         left -= n;
       }
-      if (!ok) raise_timeout(P.err, abort_flag);
-      mma_commit(drain);
-      if (!mbar_wait_poll(drain, 0, wait_ns, nullptr)) atomicOr(P.err, kErrTimeout);
+      if (!ok && lane == 0) raise_timeout(P.err, abort_flag);
+      commit_elected(drain(slot));
+      if (!mbar_wait_poll(drain(slot), 0, wait_ns, nullptr) && lane == 0) atomicOr(P.err, kErrTimeout);
     } else if (warp == 13) {
       // ===================================================== bulk copies
       struct Blocks {                             // of 32 blocks, one per lane
@@ -679,6 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t sbuf = lane_base + C::s_col(slot), obuf = lane_base + C::o_col(slot);
     uint32_t sn = 0, parts = 0;                         // S tiles and parts of this slot so far
+    uint32_t turns = 0;                                 // tiles that both slots had rows in
     bool ok = true;
     // This slot's rows of a part's Q into shared memory (zeros where there is
     // no row), scaled; returns what the row's scores are to be multiplied by.
@@ -745,8 +768,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
     }
     while (more && ok) {
       int j0, n, all_lo, all_end;
+      bool paired;
       {
         const Seg g = kept_seg();
+        paired = g.two;
         j0 = g.all.first + g.t0;
         n = g.t1 - g.t0;
         const CacheRow row = row_of(g);
@@ -771,8 +796,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
           }
           ++sn;
           tc_fence_after();
-          uint32_t sv[64], sw[64];
-          tmem_ld64_async(sbuf, sv);
           const float4 sc = scales[(tile_no + t) % 8];
           const int kb = (j0 + t) * kTile;
           // Halves outside some row's range: scores there become -inf, in
@@ -797,21 +820,21 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
               tmem_st32(sbuf + c0, s32);
             }
             tmem_st_wait();
-            tmem_ld64_async(sbuf, sv);
           }
-          // Pass 1: the row's maxima.  The second half's scores stay in
-          // registers; the first half's are read again in pass 2.
-          tmem_arrived();
-          tmem_ld64_async(sbuf + 64, sw);               // travels while the first half is reduced
-          pin64(sv);
           const float c20 = isnan(sc.x) ? 1.0f : fmaxf(c1 * sc.x, 1e-37f);   // positive: -inf stays -inf
           const float c21 = isnan(sc.y) ? 1.0f : fmaxf(c1 * sc.y, 1e-37f);
           const float ev0 = isnan(sc.z) ? 0.0f : pow2_log(sc.z), ev1 = isnan(sc.w) ? 0.0f : pow2_log(sc.w);
           ev_top = fmaxf(ev_top, fmaxf(ev0, ev1));
-          const float s0 = max64(sv) * c20;
-          tmem_arrived();
-          pin64(sw);
-          const float s1 = max64(sw) * c21;
+          // Pass 1: the row's maxima.  (Loops over the halves are rolled up: the
+          // warps' loops share one instruction cache.)
+          float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll 1
+          for (int x = 0; x < 2; ++x) {
+            uint32_t sv[64];
+            tmem_ld64(sbuf + 64 * x, sv);
+            s0 = s1;
+            s1 = max64(sv) * (x ? c21 : c20);
+          }
           const float pm = fmaxf(s0 + ev0, s1 + ev1);
           float f = 1.0f;
           if (pm > mt + 8.0f) {
@@ -852,8 +875,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
           const bool far0 = ev_top - ev0 > 90.0f, far1 = ev_top - ev1 > 90.0f;
           if (far1) far_sum(1, c21);
           if (far0) far_sum(0, c20);
-          // Pass 2: 32 scores as 16 pairs of P, at columns 64 and up of S (the
-          // second half's scores have left them).
+          // Pass 2: 32 scores as 16 pairs of P, over columns of S that have been
+          // read.
           auto weights = [&](const uint32_t* v, uint64_t c22, uint64_t off, uint32_t to, uint64_t& sum0, uint64_t& sum1) {
             uint32_t pk[16];
 #pragma unroll
@@ -879,33 +902,40 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
             __syncwarp();
             if (lane == 0) mbar_arrive(to);
           };
-          uint64_t sum1a = 0, sum1b = 0, sum0a = 0, sum0b = 0;
-          {
-            const uint64_t c22 = pack2(c21, c21), off = pack2(nm + ev1, nm + ev1);
-            weights(sw, c22, off, sbuf + 96, sum1a, sum1b);
-            tmem_ld32_async(sbuf, sv);
-            weights(sw + 32, c22, off, sbuf + 112, sum1a, sum1b);
-            hand_over(p_half(slot));
+          // The two slots' warps of one scheduler take turns at the
+          // exponentials: 128 of them are 1024 cycles of its unit, and a warp
+          // that has them alone hands its P over while the other one's
+          // products run, instead of both at half the speed.
+          if (paired) {
+            if ((slot == 1 || turns > 0) &&
+                !__all_sync(0xffffffffu, mbar_wait_poll(turn(warp), (turns - (1 - slot)) & 1u, wait_ns, abort_flag))) {
+              ok = false;
+              break;
+            }
+            ++turns;
           }
-          {
-            const uint64_t c22 = pack2(c20, c20), off = pack2(nm + ev0, nm + ev0);
+          uint32_t sa[32], sb[32];
+          tmem_ld32_async(sbuf, sa);
+#pragma unroll 1
+          for (int x = 0; x < 2; ++x) {
+            const float c2 = x ? c21 : c20, ev = x ? ev1 : ev0;
+            const uint64_t c22 = pack2(c2, c2), off = pack2(nm + ev, nm + ev);
+            uint64_t sum0 = 0, sum1 = 0;
             tmem_arrived();
-            pin32(sv);
-            tmem_ld32_async(sbuf + 32, sv + 32);
-            weights(sv, c22, off, sbuf + 64, sum0a, sum0b);
+            pin32(sa);
+            tmem_ld32_async(sbuf + 64 * x + 32, sb);
+            weights(sa, c22, off, sbuf + 32 * x, sum0, sum1);
             tmem_arrived();
-            pin32(sv + 32);
-            weights(sv + 32, c22, off, sbuf + 80, sum0a, sum0b);
-            hand_over(p_full(slot));
-          }
-          // The sums are not on the way to the next product.
-          auto take_sum = [&](uint64_t a, uint64_t b, bool far, float ev) {
+            pin32(sb);
+            if (x == 0) tmem_ld32_async(sbuf + 64, sa);
+            weights(sb, c22, off, sbuf + 32 * x + 16, sum0, sum1);
+            if (x == 1 && paired && lane == 0) mbar_arrive(turn(warp ^ 4));
+            hand_over(x ? p_full(slot) : p_half(slot));
+            // The sum is not on the way to the next product.
             float u0, u1;
-            unpack2(add2(a, b), u0, u1);
-            if (!far) add = fmaf(u0 + u1, ex2_ftz(ns - nm - ev), add);
-          };
-          take_sum(sum1a, sum1b, far1, ev1);
-          take_sum(sum0a, sum0b, far0, ev0);
+            unpack2(add2(sum0, sum1), u0, u1);
+            if (!(x ? far1 : far0)) add = fmaf(u0 + u1, ex2_ftz(ns - nm - ev), add);
+          }
           l += add;
         }
         if (!ok) break;
