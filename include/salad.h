@@ -379,7 +379,7 @@ salad_status salad_rope(const salad_rope_args* args, salad_stream stream);
  *   page_table        int32 [B, blocks]: page of block j of sequence b
  *   seq               int32 [B, 2]: tokens held (>= 0), tail slot (0 or 1)
  * All are device pointers, contiguous, the pages and tails 16-byte aligned.
- * d is 64 or 128.  An appended chunk goes to the other tail slot when it
+ * d is 64 or 128, pages * H below 2^31.  An appended chunk goes to the other tail slot when it
  * closes the open block, so (seq, tail) still describe the cache as it was:
  * a chunk may be appended again at the same seq (each denoising step of a
  * chunk does) and is kept by taking seq_out for the next seq.

@@ -240,6 +240,20 @@ bool make_tmap_bf16_2d(CUtensorMap* map, const void* base, int rows, int cols) {
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A pool of e4m3 half pages, [slabs][64][d] bytes viewed as 3-D (d, 64, slabs),
+// box d x 32 x 1: 32 keys of one page and head, swizzled over rows of d bytes.
+bool make_tmap_codes(CUtensorMap* map, const void* base, long long slabs, int d) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr || slabs > 0x7fffffffll) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), 64, static_cast<cuuint64_t>(slabs)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(d) * 64};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(d), 32, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // ------------------------------------------------------- forward layout --
 struct FwdLayout {
   size_t gate, s, sel, idx, lists, counts, lin, hst, z, g, olin, qp, kp, vp, total;
@@ -902,7 +916,9 @@ salad_status check_cache(const salad_cache& c) {
       static_cast<long long>(c.B) * c.H > 65535)
     return SALAD_ERR_INVALID_ARG;
   if (c.d != 64 && c.d != 128) return SALAD_ERR_UNSUPPORTED;
-  if (c.pages < 1 || c.blocks < 1 || c.blocks > (1 << 24)) return SALAD_ERR_INVALID_ARG;
+  if (c.pages < 1 || c.blocks < 1 || c.blocks > (1 << 24) ||
+      static_cast<long long>(c.pages) * c.H > 0x7fffffffll)
+    return SALAD_ERR_INVALID_ARG;
   if (!aligned(c.k_pages, 16) || !aligned(c.v_pages, 16) || !aligned(c.k_tail, 16) ||
       !aligned(c.v_tail, 16) || !aligned(c.k_scale, 4) || !aligned(c.v_scale, 4) ||
       !aligned(c.page_table, 4))

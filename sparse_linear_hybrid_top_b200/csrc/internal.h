@@ -154,6 +154,9 @@ bool make_tmap_bf16_heads4d(CUtensorMap* map, const void* base, int B, int H, in
 // lands box_pos whole positions, F rows each, in space-major order.
 bool make_tmap_bf16_regroup(CUtensorMap* map, const void* base, int S, int F, int npos, int d,
                             int box_pos);
+// Half pages of an e4m3 pool [slabs][64][d]: box d x 32 x 1, swizzled over its
+// rows (128-byte at d = 128, 64-byte at d = 64).
+bool make_tmap_codes(CUtensorMap* map, const void* base, long long slabs, int d);
 bool make_tmap_bf16_2d(CUtensorMap* map, const void* base, int rows, int cols);
 
 // ---- full-width projections (proj.cu)
