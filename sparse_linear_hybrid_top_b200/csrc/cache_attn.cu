@@ -678,16 +678,20 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const __grid_const
   }
 }
 
-// Merges the parts of the sequences that more than one CTA worked on: a warp
-// per row.
+// Merges the parts of the sequences that more than one CTA worked on: a CTA
+// per row, whose warps take a quarter of its parts each.
+constexpr int kMergeLane = 3;          // parts of a lane
+constexpr int kMaxParts = 4 * 32 * kMergeLane;
 template <int D>
 __global__ void __launch_bounds__(kThreads) cache_merge_kernel(const __grid_constant__ CacheAttnParams P, int rows, int slots) {
-  const int lane = threadIdx.x % 32;
-  const long long row = static_cast<long long>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
+  constexpr int C = D / 32;
+  constexpr int FLY = 16;              // parts whose loads are in flight
+  __shared__ float os[4][D];
+  __shared__ float2 mls[4];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int used = P.group * P.N;      // of the `rows` that a part holds
+  const int r = blockIdx.x % used, h = blockIdx.x / used % P.c.H, b = blockIdx.x / used / P.c.H;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (row >= static_cast<long long>(P.c.B) * P.c.H * rows) return;
-  const int r = static_cast<int>(row % rows), h = static_cast<int>(row / rows % P.c.H);
-  const int b = static_cast<int>(row / rows / P.c.H);
   const long long w0 = P.plan[b], w1 = P.plan[b + 1], total = P.plan[P.c.B];
   if (w0 == w1) return;
   const long long ctas = run_ctas(total, slots);
@@ -699,41 +703,62 @@ __global__ void __launch_bounds__(kThreads) cache_merge_kernel(const __grid_cons
   const int count = P.counts == nullptr ? P.N : cache_count(__ldg(P.counts + b), P.N, &bad);
   const int i_q = r / P.group, head = h * P.group + r % P.group;
   if (i_q >= count) return;
-  const long long at = (static_cast<long long>(x0 + b) * P.c.H + h) * rows + r, step = static_cast<long long>(P.c.H) * rows;
-  // Four parts a lane (128 at most): a part's weight against the largest
-  // maximum, 0 where it saw no key (its O is 0 too).
-  float2 p[4];
+  const int k0 = n * warp / 4, nw = n * (warp + 1) / 4 - k0;
+  const long long step = static_cast<long long>(P.c.H) * rows;
+  const long long at = (static_cast<long long>(x0 + b + k0) * P.c.H + h) * rows + r;
+  const float* from = P.part_o + at * D + lane * C;
+  float v[FLY][C];
+  auto load = [&](int k) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    p[i] = lane + 32 * i < n ? P.part_ml[at + (lane + 32 * i) * step] : make_float2(-INFINITY, 0.0f);
-  float mm = fmaxf(fmaxf(p[0].x, p[1].x), fmaxf(p[2].x, p[3].x));
+    for (int i = 0; i < FLY; ++i)
+#pragma unroll
+      for (int c = 0; c < C; ++c) v[i][c] = k + i < nw ? from[(k + i) * step * D + c] : 0.0f;
+  };
+  load(0);
+  // A part's weight against the warp's largest maximum, 0 where it saw no key
+  // (its O is 0 too).
+  float2 p[kMergeLane];
+  float mm = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kMergeLane; ++i) {
+    p[i] = lane + 32 * i < nw ? P.part_ml[at + (lane + 32 * i) * step] : make_float2(-INFINITY, 0.0f);
+    mm = fmaxf(mm, p[i].x);
+  }
 #pragma unroll
   for (int i = 16; i > 0; i /= 2) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, i));
-  float w[4], ll = 0.0f;
+  auto weight = [](float2 x, float top) { return x.y == 0.0f ? 0.0f : (x.x == -INFINITY ? 1.0f : ex2_ftz(x.x - top)); };
+  float ll = 0.0f, acc[C] = {};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    w[i] = p[i].y == 0.0f ? 0.0f : (p[i].x == -INFINITY ? 1.0f : ex2_ftz(p[i].x - mm));
-    ll = fmaf(p[i].y, w[i], ll);
+  for (int i = 0; i < kMergeLane; ++i) {
+    const float w = weight(p[i], mm);
+    ll = fmaf(p[i].y, w, ll);
+    for (int k = 32 * i; k < min(nw, 32 * i + 32); k += FLY) {
+      if (k > 0) load(k);
+#pragma unroll
+      for (int j = 0; j < FLY; ++j) {
+        const float f = __shfl_sync(0xffffffffu, w, (k + j) % 32);
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc[c] = fmaf(v[j][c], f, acc[c]);
+      }
+    }
   }
 #pragma unroll
   for (int i = 16; i > 0; i /= 2) ll += __shfl_xor_sync(0xffffffffu, ll, i);
-  constexpr int C = D / 32;
-  float acc[C] = {};
-  const float* from = P.part_o + at * D + lane * C;
-  // Eight parts' loads in flight.
-  for (int k0 = 0; k0 < n; k0 += 8) {
-    float v[8][C];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+  for (int c = 0; c < C; ++c) os[warp][lane * C + c] = acc[c];
+  if (lane == 0) mls[warp] = make_float2(mm, ll);
+  __syncthreads();
+  if (warp > 0) return;
+  mm = fmaxf(fmaxf(mls[0].x, mls[1].x), fmaxf(mls[2].x, mls[3].x));
+  ll = 0.0f;
 #pragma unroll
-      for (int c = 0; c < C; ++c) v[i][c] = k0 + i < n ? from[(k0 + i) * step * D + c] : 0.0f;
-    const float wk = k0 < 32 ? w[0] : (k0 < 64 ? w[1] : (k0 < 96 ? w[2] : w[3]));
+  for (int c = 0; c < C; ++c) acc[c] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float f = __shfl_sync(0xffffffffu, wk, (k0 + i) % 32);
+  for (int k = 0; k < 4; ++k) {
+    const float f = weight(mls[k], mm);
+    ll = fmaf(mls[k].y, f, ll);
 #pragma unroll
-      for (int c = 0; c < C; ++c) acc[c] = fmaf(v[i][c], f, acc[c]);
-    }
+    for (int c = 0; c < C; ++c) acc[c] = fmaf(os[k][lane * C + c], f, acc[c]);
   }
   const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
   char* to = P.o + b * P.ob + head * P.oh + i_q * P.on + 2 * lane * C;
@@ -756,12 +781,12 @@ Shape shape_of(const CacheAttnArgs& a, int num_sms) {
   const long long rows = static_cast<long long>(a.Hq / H) * a.N;
   s.rw = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
   // One wave of two CTAs to an SM, each with eight half pages at the least (of
-  // a full table); 128 parts of a sequence at most, which is what a merging
-  // warp holds.  Past kScan sequences a CTA takes one of them each.
+  // a full table); kMaxParts of a sequence at most, which is what the merge
+  // holds.  Past kScan sequences a CTA takes one of them each.
   long long slots = 2ll * num_sms / H;
   const long long most = (B * (2ll * a.cache.blocks + 2) + 7) / 8;
   if (slots > most) slots = most;
-  if (slots > 128) slots = 128;
+  if (slots > kMaxParts) slots = kMaxParts;
   if (slots < 1) slots = 1;
   s.merge = B <= kScan && slots > 1;
   s.slots = B <= kScan ? static_cast<int>(slots) : B;
@@ -800,10 +825,10 @@ template <int D>
 cudaError_t launch_d(const Ctx& c, const CacheAttnParams& P, const Shape& s) {
   const cudaError_t e = s.rw == 1 ? launch_rw<D, 1>(c, P, s) : (s.rw == 2 ? launch_rw<D, 2>(c, P, s) : launch_rw<D, 4>(c, P, s));
   if (e != cudaSuccess || !s.merge) return e;
-  const long long rows = static_cast<long long>(P.c.B) * P.c.H * s.rw * 16;
+  const long long rows = static_cast<long long>(P.c.B) * P.c.H * P.group * P.N;
   // Launched while the attention runs; it waits for its end before it reads.
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + kThreads / 32 - 1) / (kThreads / 32)));
+  cfg.gridDim = dim3(static_cast<unsigned>(rows));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = c.stream;
   cudaLaunchAttribute early = {};
