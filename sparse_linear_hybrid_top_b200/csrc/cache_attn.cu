@@ -224,11 +224,11 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const __grid_const
     const int part1 = w1 - from_b < s.n ? static_cast<int>(w1 - from_b) : s.n;
     const bool whole = part0 == 0 && part1 == s.n;
 
-    // This group's half pages [u0, u1): its share of the CTA's part.
-    const int u0 = s.first + part0 + (part1 - part0) * kw / KW;
-    const int u1 = s.first + part0 + (part1 - part0) * (kw + 1) / KW;
-    const int closed = 2 * (s.len / kCacheBlock);       // half pages of closed blocks
-    const int uc = min(u1, closed);
+    // This group's half pages: u0 + KW i below u1, of which the first nc are of
+    // closed blocks.  Taken in turn, the open block's two go to two groups.
+    const int u0 = s.first + part0 + kw, u1 = s.first + part1;
+    const int uc = min(u1, 2 * (s.len / kCacheBlock));
+    const int nc = max(0, (uc - u0 + KW - 1) / KW);
     unsigned char* stages = ring + static_cast<size_t>(kw) * NST * 2 * R::kHalf;
     const int32_t* table = P.c.page_table + static_cast<long long>(b) * P.c.blocks;
     // Pages and scales of the 32 blocks from block `first` on, one per lane (-1:
@@ -274,12 +274,13 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const __grid_const
       for (int i = 0; i < 2; ++i) qx[x][i] = query(w, (e / 32) % KS, l, i);
     }
     if (threadIdx.x < ROWS) q_top[threadIdx.x] = 0;
-    // Half page u's copies (by the group's first warp); a block without a page
+    // Half page i's copies (by the group's first warp); a block without a page
     // reads page 0, and is masked.
-    auto fetch = [&](int u, const Blocks& x) {
+    auto fetch = [&](int i, const Blocks& x) {
+      const int u = u0 + KW * i;
       const int page = __shfl_sync(0xffffffffu, x.page, (u / 2 - b0) % 32);
       if (rt == 0 && lane == 0) {
-        const int st = (done + u - u0) % NST;
+        const int st = (done + i) % NST;
         const int slab = (page < 0 ? 0 : page) * P.c.H + h;
         const uint32_t dst = smem_u32(stages) + st * 2 * R::kHalf;
         mbar_arrive_expect_tx(landed(st), 2 * R::kHalf);
@@ -289,10 +290,10 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const __grid_const
     };
     // Block groups of 32 that `cur` and `nxt` hold: in_cur is the first one's number.
     int in_cur = 0;
-    auto blocks_of = [&](int u) -> const Blocks& { return (u / 2 - b0) / 32 == in_cur ? cur : nxt; };
-    static_assert(NST <= 62, "the ring stays within two groups of blocks");
-    int issued = u0;
-    for (; issued < uc && issued < u0 + NST; ++issued) fetch(issued, blocks_of(issued));
+    auto blocks_of = [&](int i) -> const Blocks& { return ((u0 + KW * i) / 2 - b0) / 32 == in_cur ? cur : nxt; };
+    static_assert(NST * KW <= 62, "the ring stays within two groups of blocks");
+    int issued = 0;
+    for (; issued < nc && issued < NST; ++issued) fetch(issued, blocks_of(issued));
     __syncthreads();
 #pragma unroll
     for (int x = 0; x < QE; ++x) {
@@ -409,8 +410,10 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const __grid_const
     };
 
     // ---- closed blocks
-    for (int u = u0; u < uc; ++u) {
-      const int st = (done + u - u0) % NST;
+    for (int n = 0; n < nc; ++n) {
+      const int u = u0 + KW * n;
+      const int st = (done + n) % NST;
+      const uint32_t phase = static_cast<uint32_t>((done + n) / NST) & 1u;
       if ((u / 2 - b0) / 32 != in_cur) {
         cur = nxt;
         ++in_cur;
@@ -419,7 +422,7 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const __grid_const
       const int at = (u / 2 - b0) % 32;
       const bool none = __shfl_sync(0xffffffffu, cur.page, at) < 0;
       const float ks = __shfl_sync(0xffffffffu, cur.ks, at), vs = __shfl_sync(0xffffffffu, cur.vs, at);
-      if (!__all_sync(0xffffffffu, mbar_wait_poll(landed(st), static_cast<uint32_t>((done + u - u0) / NST) & 1u, P.wait_ns, nullptr))) {
+      if (!__all_sync(0xffffffffu, mbar_wait_poll(landed(st), phase, P.wait_ns, nullptr))) {
         ok = false;
         break;
       }
@@ -472,9 +475,9 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const __grid_const
       // every warp of the group says so.
       __syncwarp();
       if (RW > 1 && lane == 0) mbar_arrive(freed(st));
-      if (issued < uc) {
+      if (issued < nc) {
         if (RW > 1 && rt == 0 &&
-            !__all_sync(0xffffffffu, mbar_wait_poll(freed(st), static_cast<uint32_t>((done + u - u0) / NST) & 1u, P.wait_ns, nullptr))) {
+            !__all_sync(0xffffffffu, mbar_wait_poll(freed(st), phase, P.wait_ns, nullptr))) {
           ok = false;
           break;
         }
@@ -505,13 +508,13 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const __grid_const
     // No copy may be in flight when the ring is used again, or at the exit: each
     // one issued is waited for here, unless the loop above has seen it land.
     if (!ok && rt == 0)
-      for (int u = max(u0, issued - NST); u < issued; ++u)
-        mbar_wait_poll(landed((done + u - u0) % NST), static_cast<uint32_t>((done + u - u0) / NST) & 1u, P.wait_ns, nullptr);
-    done += max(0, uc - u0);
+      for (int n = max(0, issued - NST); n < issued; ++n)
+        mbar_wait_poll(landed((done + n) % NST), static_cast<uint32_t>((done + n) / NST) & 1u, P.wait_ns, nullptr);
+    done += nc;
 
-    // ---- the open block, in bf16 (at most two half pages of one group).  All
+    // ---- the open block, in bf16 (at most two half pages).  All
     // loads of a half page are issued before the first is used.
-    for (int u = max(u0, closed); u < u1 && ok; ++u) {
+    for (int u = u0 + KW * nc; u < u1 && ok; u += KW) {
       const long long at = (((static_cast<long long>(b) * 2 + s.slot) * P.c.H + h) * kCacheBlock + (u & 1) * 32) * D;
       const __nv_bfloat16* kt = static_cast<const __nv_bfloat16*>(P.c.k_tail) + at;
       const __nv_bfloat16* vt = static_cast<const __nv_bfloat16*>(P.c.v_tail) + at;
