@@ -24,7 +24,7 @@ struct CacheAttnParams {
   int tiles;                          // row tiles of one (sequence, key head)
   float* part_o;                      // unnormalised parts of rows, for the merging launch
   float2* part_ml;                    // their maxima and sums
-  long long* plan;                    // [B + 1], prefix sums of the sequences' work
+  int2* plan;                         // [B], first CTA of a sequence's parts, and how many
   unsigned* err;
   unsigned long long wait_ns;
 };
