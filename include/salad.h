@@ -379,10 +379,11 @@ salad_status salad_rope(const salad_rope_args* args, salad_stream stream);
  *   page_table        int32 [B, blocks]: page of block j of sequence b
  *   seq               int32 [B, 2]: tokens held (>= 0), tail slot (0 or 1)
  * All are device pointers, contiguous, the pages and tails 16-byte aligned.
- * d is 64 or 128, pages * H below 2^31.  An appended chunk goes to the other tail slot when it
- * closes the open block, so (seq, tail) still describe the cache as it was:
- * a chunk may be appended again at the same seq (each denoising step of a
- * chunk does) and is kept by taking seq_out for the next seq.
+ * d is 64 or 128, pages * H below 2^31.  An appended chunk goes to the other
+ * tail slot when it closes the open block, so (seq, tail) still describe the
+ * cache as it was: a chunk may be appended again at the same seq (each
+ * denoising step of a chunk does) and is kept by taking seq_out for the next
+ * seq.
  * Pages that a call writes must differ from one another and from the pages
  * of blocks that are to be kept.
  * Table entries that are read and lie outside [0, pages) are skipped on the
@@ -412,7 +413,7 @@ typedef struct salad_cache {
  * k, v: bf16 [B,H,N,d] with strides as in salad_rope.  counts: int32 [B]
  * device or NULL (N each); rows behind a count are not read.
  * seq_out: int32 [B,2], seq after the append; may be seq itself (a second,
- * small launch advances it then) and may be NULL.
+ * small launch advances it then) and may be NULL; it overlaps nothing else.
  */
 typedef struct salad_cache_append_args {
     salad_cache cache;
@@ -449,10 +450,14 @@ salad_status salad_cache_append(const salad_cache_append_args* args, salad_strea
  * q, o: bf16 [B,Hq,N,d], strides as in salad_rope; Hq a multiple of the
  * cache's H, query head h reading key/value head h / (Hq / H).  lse (may be
  * NULL): float32 [B,Hq,N] contiguous, natural log of the sum of exponentials.
- * Rows behind a count are left as they are.  o must not overlap q.
- * Closed blocks are read as their exact values (code * scale); softmax
- * statistics and sums are float32, P is rounded to bf16 for the product with
- * the values.  Workspace: salad_cache_attn_workspace_bytes(args); two calls
+ * Rows behind a count are left as they are.  o and lse overlap nothing else.
+ * Closed blocks are read as their exact values (code * scale), so scales are
+ * powers of two from 2^-100 up, or NaN with NaN codes, as the append writes
+ * them.  Softmax statistics and sums are float32.  P is rounded for the
+ * product with the values: to fp16 (by 2^-11 of itself; what is below 2^-14 of
+ * a row's largest product of weight and block scale, by 2^-25 of that), and in
+ * calls of up to 64 rows of a key head to bf16 with the open block's values.
+ * (Rows of a key head / 256) * (blocks / 2) stays below 2^31.  Workspace: salad_cache_attn_workspace_bytes(args); two calls
  * that may overlap on the GPU need two workspaces.
  */
 typedef struct salad_cache_attn_args {

@@ -838,6 +838,14 @@ bool disjoint(const Strided& a, const Strided& b) {
   return false;
 }
 
+// Whether a tensor lies clear of n bytes at p (NULL: none).
+bool clear_of(const Strided& t, const void* p, size_t n) {
+  return p == nullptr || !overlaps(t.base, static_cast<size_t>(t.extent()), p, n);
+}
+
+// Bytes of a rotation's positions.
+size_t position_bytes(int batched, int B, int N) { return (batched ? static_cast<size_t>(B) : 1u) * N * 12; }
+
 bool same_place(const Strided& a, const Strided& b) {
   if (a.base != b.base) return false;
   for (int i = 0; i < 3; ++i)
@@ -886,6 +894,8 @@ salad_status salad_rope(const salad_rope_args* a, salad_stream stream) {
   for (int i = 0; i < sides; ++i) {
     if (!strides_ok(in[i]) || !strides_ok(out[i]) || !distinct(out[i])) return SALAD_ERR_INVALID_ARG;
     if (!same_place(in[i], out[i]) && !disjoint(in[i], out[i])) return SALAD_ERR_INVALID_ARG;
+    if (!clear_of(out[i], a->positions, position_bytes(a->positions_batched, a->B, a->N)))
+      return SALAD_ERR_INVALID_ARG;
   }
   if (sides == 2 && (!disjoint(out[0], out[1]) || !disjoint(out[0], in[1]) || !disjoint(out[1], in[0])))
     return SALAD_ERR_INVALID_ARG;
@@ -940,6 +950,11 @@ CacheView cache_view(const salad_cache& c) {
   return v;
 }
 
+// Contiguous memory as a tensor of one row.
+Strided flat(const void* p, size_t bytes) {
+  return Strided{static_cast<const char*>(p), {1, 1, 1}, {0, 0, 0}, static_cast<long long>(bytes)};
+}
+
 // Whether a tensor shares memory with one of the cache's buffers.
 bool in_cache(const salad_cache& c, const Strided& t) {
   const size_t page = static_cast<size_t>(c.pages) * c.H * 64 * c.d;
@@ -948,7 +963,8 @@ bool in_cache(const salad_cache& c, const Strided& t) {
   const size_t n = static_cast<size_t>(t.extent());
   return overlaps(t.base, n, c.k_pages, page) || overlaps(t.base, n, c.v_pages, page) ||
          overlaps(t.base, n, c.k_tail, tail) || overlaps(t.base, n, c.v_tail, tail) ||
-         overlaps(t.base, n, c.k_scale, scale) || overlaps(t.base, n, c.v_scale, scale);
+         overlaps(t.base, n, c.k_scale, scale) || overlaps(t.base, n, c.v_scale, scale) ||
+         overlaps(t.base, n, c.page_table, static_cast<size_t>(c.B) * c.blocks * 4);
 }
 
 }  // namespace
@@ -960,11 +976,14 @@ salad_status salad_cache_append(const salad_cache_append_args* a, salad_stream s
   if (st != SALAD_OK) return st;
   if (a->N < 1 || a->N > kMaxN) return SALAD_ERR_INVALID_ARG;
   if (!aligned(a->seq, 4)) return SALAD_ERR_INVALID_ARG;
-  if (a->seq_out != nullptr &&
-      (!aligned(a->seq_out, 4) ||
-       (a->seq_out != a->seq &&
-        overlaps(a->seq_out, static_cast<size_t>(cc.B) * 8, a->seq, static_cast<size_t>(cc.B) * 8))))
-    return SALAD_ERR_INVALID_ARG;
+  const size_t seq_bytes = static_cast<size_t>(cc.B) * 8;
+  if (a->seq_out != nullptr) {
+    const Strided to = flat(a->seq_out, seq_bytes);
+    if (!aligned(a->seq_out, 4) || in_cache(cc, to) || (a->seq_out != a->seq && !clear_of(to, a->seq, seq_bytes)) ||
+        !clear_of(to, a->counts, seq_bytes / 2) ||
+        (a->rotate && !clear_of(to, a->positions, position_bytes(a->positions_batched, cc.B, a->N))))
+      return SALAD_ERR_INVALID_ARG;
+  }
   if (a->counts != nullptr && !aligned(a->counts, 4)) return SALAD_ERR_INVALID_ARG;
   if (a->rotate != 0 && a->rotate != 1) return SALAD_ERR_INVALID_ARG;
   if (a->rotate &&
@@ -973,7 +992,8 @@ salad_status salad_cache_append(const salad_cache_append_args* a, salad_stream s
     return st;
   const Strided k = strided(a->k, a->k_st, cc.B, cc.H, a->N, cc.d * 2, 2);
   const Strided v = strided(a->v, a->v_st, cc.B, cc.H, a->N, cc.d * 2, 2);
-  if (!strides_ok(k) || !strides_ok(v) || in_cache(cc, k) || in_cache(cc, v))
+  if (!strides_ok(k) || !strides_ok(v) || in_cache(cc, k) || in_cache(cc, v) ||
+      (a->seq_out != nullptr && (!clear_of(k, a->seq_out, seq_bytes) || !clear_of(v, a->seq_out, seq_bytes))))
     return SALAD_ERR_INVALID_ARG;
   Ctx c;
   if ((st = get_ctx(stream, &c)) != SALAD_OK) return st;
@@ -1014,14 +1034,17 @@ salad_status check_cache_attn(const salad_cache_attn_args* a, CacheAttnArgs* p) 
   if (a->frame < 0 || !(a->scale > 0.0f) || !std::isfinite(a->scale)) return SALAD_ERR_INVALID_ARG;
   const Strided q = strided(a->q, a->q_st, cc.B, a->Hq, a->N, cc.d * 2, 2);
   const Strided o = strided(a->o, a->o_st, cc.B, a->Hq, a->N, cc.d * 2, 2);
-  if (!strides_ok(q) || !strides_ok(o) || !distinct(o) || !disjoint(q, o) || in_cache(cc, o))
-    return SALAD_ERR_INVALID_ARG;
-  if (a->lse != nullptr) {
-    const size_t n = static_cast<size_t>(cc.B) * a->Hq * a->N * 4;
-    if (overlaps(a->lse, n, q.base, static_cast<size_t>(q.extent())) ||
-        overlaps(a->lse, n, o.base, static_cast<size_t>(o.extent())))
+  if (!strides_ok(q) || !strides_ok(o) || !distinct(o) || !disjoint(q, o)) return SALAD_ERR_INVALID_ARG;
+  const size_t lse_bytes = static_cast<size_t>(cc.B) * a->Hq * a->N * 4;
+  if (!clear_of(q, a->lse, lse_bytes) || !clear_of(o, a->lse, lse_bytes)) return SALAD_ERR_INVALID_ARG;
+  const Strided outs[2] = {o, flat(a->lse, lse_bytes)};
+  for (int i = 0; i < (a->lse != nullptr ? 2 : 1); ++i)
+    if (in_cache(cc, outs[i]) || !clear_of(outs[i], a->seq, static_cast<size_t>(cc.B) * 8) ||
+        !clear_of(outs[i], a->counts, static_cast<size_t>(cc.B) * 4))
       return SALAD_ERR_INVALID_ARG;
-  }
+  // Key tiles of a sequence's rows are counted in 32 bits.
+  const long long items = (static_cast<long long>(a->Hq / cc.H) * a->N + 255) / 256;
+  if (items * (cc.blocks / 2 + 1) > 0x7fffffffll) return SALAD_ERR_UNSUPPORTED;
   std::memset(p, 0, sizeof(*p));
   p->cache = cache_view(cc);
   p->seq = a->seq;

@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
         }
         commit_elected(s_full(slot));
       };
-      int left = static_cast<int>(w1 - w0);
+      long long left = w1 - w0;
       for (int part_no = 0; left > 0; ++part_no) {
         if (!(ok = wait(full(st), ph))) break;
         const int2 info = part_info[part_no % 8];
@@ -542,7 +542,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
         }
         return tail_scale(__reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16)));
       };
-      uint32_t at = 0, tile_no = 0;               // operand tiles and key tiles so far
+      unsigned long long at = 0;                  // operand tiles so far
+      uint32_t tile_no = 0;                       // key tiles so far
       int part_no = 0;
       bool ok = true;
       for (Seg g = seg_at(T, w0, w1 - w0); g.left > 0 && ok; g = seg_next(P, g), ++part_no) {
@@ -567,8 +568,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
 #pragma unroll 1
           for (int value = 0; value < 2 && ok; ++value, ++at) {
             const int rs = static_cast<int>(at % NR);
-            const uint32_t n = at / NR;
-            ok = n == 0 || __all_sync(0xffffffffu, mbar_wait_poll(raw_empty(rs), (n - 1) & 1u, wait_ns, abort_flag));
+            const unsigned long long n = at / NR;
+            ok = n == 0 || __all_sync(0xffffffffu, mbar_wait_poll(raw_empty(rs), static_cast<uint32_t>(n - 1) & 1u, wait_ns, abort_flag));
             if (!ok) break;
             if (lane == 0) {
               if (!value) {
@@ -590,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
       // No bulk copy may be in flight at the exit.
       if (lane == 0) {
         for (uint32_t i = 0; i < NR && i < at; ++i) {
-          const uint32_t last = (at - 1 - i) / NR;            // turns of raw slot i, less one
+          const uint32_t last = static_cast<uint32_t>((at - 1 - i) / NR);            // turns of raw slot i, less one
           if (!mbar_wait_poll(raw_full(static_cast<int>(i)), last & 1u, wait_ns, nullptr)) atomicOr(P.err, kErrTimeout);
         }
       }

@@ -314,3 +314,11 @@ def test_append_refusals_on_the_device():
     with pytest.raises(ValueError):
         salad.BlockCache(cache.k_pages.view(torch.uint8), cache.v_pages, cache.k_scale, cache.v_scale, cache.k_tail,
                          cache.v_tail, cache.page_table)
+
+
+def test_seq_out_apart_from_inputs():
+    """seq_out may be seq; it may not lie in counts, positions, the cache, k or v."""
+    at = A + 7 * M + 256
+    for kw in (dict(k=at), dict(v=at), dict(counts=at), dict(positions=at), dict(seq_out=A), dict(seq_out=A + 3 * M),
+               dict(seq_out=A + 4 * M), dict(seq_out=A + 6 * M)):
+        assert _status(**kw) == INVALID, kw

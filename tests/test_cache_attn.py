@@ -443,3 +443,86 @@ def test_attn_refusals_on_the_device():
         with pytest.raises(salad.SaladError) as e:
             salad.cache_attn(**{**dict(cache=cache, q=q, seq=seq), **bad})
         assert e.value.code == INVALID
+
+
+def test_outputs_apart_from_inputs():
+    """o and lse may not lie in the cache, in seq or in counts."""
+    for at in (A + 2 * M, A + 4 * M, A + 6 * M, A + 7 * M):
+        assert _status(lse=at) == INVALID and _status(o=at) == INVALID
+    assert _status(counts=A + 10 * M) == INVALID
+    assert _status(counts=A + 9 * M) == INVALID
+    # Key tiles of the rows of one key head beyond 31 bits.
+    wide = dict(N=262144, Hq=3, lse=None, workspace=None, q_st=Strides(3 << 24, 1 << 24, 64), o_st=Strides(3 << 24, 1 << 24, 64))
+    assert _status(cache=dict(blocks=1 << 23), **wide) == UNSUP
+    assert _status(cache=dict(blocks=1 << 21), **wide) == WS
+
+
+@needs_gpu
+@pytest.mark.parametrize("N,Hq,H", [(1, 5, 1), (2, 4, 2), (65, 1, 1), (40, 8, 2)])
+@pytest.mark.parametrize("lens", [
+    [2111 - 131 * i for i in range(16)],
+    [0, 5000, 0, 0, 64, 1, 3000, 0, 63, 128, 0],
+    [1, 2, 3, 4, 5, 6, 7, 4001],
+])
+def test_unequal_sequences(N, Hq, H, lens):
+    """Runs of work that begin and end inside sequences, between them, and skip
+    empty ones; every other sequence has fewer rows, some none.  (Sums of up to
+    5000 keys: the bound takes n from the longest.)"""
+    cache, seq = _make(len(lens), H, 64, lens, seed=N)
+    counts = [(N, max(1, N // 2), 0)[i % 3] for i in range(len(lens))]
+    q = _q(len(lens), Hq, N, 64, 7 * N)
+    _check(cache, q, seq, frame=1)
+    _check(cache, q, seq, counts)
+
+
+@needs_gpu
+@pytest.mark.parametrize("B,N", [(512, 1), (513, 1), (513, 70)])
+def test_many_sequences(B, N):
+    """As many sequences as a CTA sums (512), and more."""
+    lens = [(i * 37) % 150 for i in range(B)]
+    cache, seq = _make(B, 1, 64, lens, seed=B)
+    counts = [N if i % 3 else i % 2 for i in range(B)]
+    _check(cache, _q(B, 1, N, 64, B), seq, counts, frame=1)
+
+
+@needs_gpu
+@pytest.mark.parametrize("Hq,N", [(1, 1), (3, 2), (1, 20), (2, 40)])
+def test_one_key_head_over_many_ctas(Hq, N):
+    """More than 128 parts of a row, of a sequence longer than its pool: many
+    blocks are the same page.  (60001 keys: n 2^-23 is 0.7%, which the bound has.)"""
+    n = 60001
+    cache, seq = _make(1, 1, 64, [2111], blocks=n // 64, seed=3)
+    cache.page_table[0] = cache.page_table[0, torch.arange(n // 64) % 32]
+    seq[0, 0] = n
+    cache.k_tail.copy_(torch.randn(cache.k_tail.shape).bfloat16())
+    cache.v_tail.copy_(torch.randn(cache.v_tail.shape).bfloat16())
+    _check(cache, _q(1, Hq, N, 64, N), seq, frame=1)
+
+
+@needs_gpu
+def test_sequences_share_pages():
+    """Two sequences with a common prefix name the same pages."""
+    cache, seq = _make(2, 2, 128, [700, 900], seed=11)
+    cache.page_table[1, :10] = cache.page_table[0, :10]
+    for N in (1, 70):
+        _check(cache, _q(2, 4, N, 128, N), seq, frame=1)
+
+
+@needs_gpu
+@pytest.mark.parametrize("N", [1, 100])
+def test_calls_at_the_same_time_on_two_streams(N):
+    """Two calls that overlap, each with a workspace of its own."""
+    cache, seq = _make(2, 4, 128, [2100, 777], seed=5)
+    q = [_q(2, 8, N, 128, s) for s in (1, 2)]
+    want = [salad.cache_attn(cache, x, seq, frame=1) for x in q]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            got[i].append(salad.cache_attn(cache, q[i], seq, frame=1, stream=s))
+    torch.cuda.synchronize()
+    salad.check_error()
+    for i in range(2):
+        for o in got[i]:
+            assert torch.equal(o, want[i])       # the split does not depend on timing

@@ -268,3 +268,8 @@ def test_rope_captured_and_on_another_stream():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, salad.rope(new, grid=(3, 5)))
+
+
+def test_rope_outputs_apart_from_positions():
+    for kw in (dict(positions=A + M), dict(positions=A + 3 * M + 64), dict(positions=A + M - 4)):
+        assert _status(Hh=0, Wh=0, **kw) == INVALID, kw
