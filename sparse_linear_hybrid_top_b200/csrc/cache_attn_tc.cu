@@ -117,6 +117,7 @@ __device__ __forceinline__ long long work_ctas(long long total, int ctas) {
 __global__ void __launch_bounds__(1024) cache_plan_kernel(const __grid_constant__ TcParams T) {
   const CacheAttnParams& P = T.a;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int b = warp; b < P.c.B; b += 32) {
     bool bad = false;
     const SeqInfo s = seq_info(P, b, &bad);
@@ -185,25 +186,25 @@ __device__ __forceinline__ Seg seg_at(const TcParams& T, long long w, long long 
   int lo = 0, hi = P.c.B;
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
-    if (__ldg(T.seq_prefix + mid) <= w) lo = mid; else hi = mid;
+    if (T.seq_prefix[mid] <= w) lo = mid; else hi = mid;
   }
   g.b = lo;
   const int* pre = T.tile_prefix + static_cast<long long>(g.b) * (P.tiles + 1);
-  const int per = __ldg(pre + P.tiles);
-  const long long rem = w - __ldg(T.seq_prefix + g.b);
+  const int per = pre[P.tiles];
+  const long long rem = w - T.seq_prefix[g.b];
   g.h = static_cast<int>(rem / per);
   const int at = static_cast<int>(rem % per);
   lo = 0;
   hi = P.tiles;
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
-    if (__ldg(pre + mid) <= at) lo = mid; else hi = mid;
+    if (pre[mid] <= at) lo = mid; else hi = mid;
   }
   g.tile = lo;
   g.left = left;
   g.first = true;
   seg_open(P, g);
-  g.t0 = at - __ldg(pre + lo);
+  g.t0 = at - pre[lo];
   seg_close(P, g);
   return g;
 }
@@ -329,7 +330,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
     if (threadIdx.x == 0) atomicOr(P.err, kErrLayout);
     return;
   }
-  const long long total = __ldg(T.seq_prefix + P.c.B);
+  // Every CTA is on an SM by then; the merge's follow as these end.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const long long total = T.seq_prefix[P.c.B];
   const long long ctas = work_ctas(total, gridDim.x);
   if (blockIdx.x >= ctas) return;
   const long long w0 = total * blockIdx.x / ctas, w1 = total * (blockIdx.x + 1) / ctas;
@@ -706,26 +710,40 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
     bool ok = true;
     // This slot's rows of a part's Q into shared memory (zeros where there is
     // no row), scaled; returns what the row's scores are to be multiplied by.
+    // A warp's rows are all in flight at once, and are scaled in their places.
     auto load_q = [&](const Seg& g) -> float {
+      constexpr int CR = D / 8;                         // 16-byte chunks of a row
       const CacheRow row = cache_row(P, g.tile * kRows + slot * 128 + r, g.h, g.s.len, g.s.count);
-      const uint4* from = reinterpret_cast<const uint4*>(P.q + g.b * P.qb + row.head * P.qh + row.n * P.qn);
-      unsigned char* to = qbuf + slot * C::kOperand + r * 128;
-      uint4 x[D / 8];
+      const unsigned long long from =
+          row.valid ? reinterpret_cast<unsigned long long>(P.q + g.b * P.qb + row.head * P.qh + row.n * P.qn) : 0ull;
+      unsigned char* buf = qbuf + slot * C::kOperand + quarter * 32 * 128;
+      auto chunk = [&](int i, int c) { return buf + (c / 8) * C::kRowSlab + i * 128 + ((c % 8 ^ (i & 7)) << 4); };
+#pragma unroll 4
+      for (int x = lane; x < 32 * CR; x += 32) {
+        const unsigned long long at = __shfl_sync(0xffffffffu, from, x / CR);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(chunk(x / CR, x % CR))),
+                     "l"(at != 0 ? at + 16 * (x % CR) : reinterpret_cast<unsigned long long>(P.q)), "r"(at != 0 ? 16 : 0)
+                     : "memory");
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
       uint32_t top = 0;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        x[i] = row.valid ? from[i] : make_uint4(0u, 0u, 0u, 0u);
-        top = __vmaxu2(__vmaxu2(top, x[i].x & 0x7fff7fffu), x[i].y & 0x7fff7fffu);
-        top = __vmaxu2(__vmaxu2(top, x[i].z & 0x7fff7fffu), x[i].w & 0x7fff7fffu);
+#pragma unroll 4
+      for (int i = 0; i < CR; ++i) {
+        const uint4 x = *reinterpret_cast<const uint4*>(chunk(lane, i));
+        top = __vmaxu2(__vmaxu2(top, x.x & 0x7fff7fffu), x.y & 0x7fff7fffu);
+        top = __vmaxu2(__vmaxu2(top, x.z & 0x7fff7fffu), x.w & 0x7fff7fffu);
       }
       top = max(top & 0xffffu, top >> 16);
       // A row with an infinity or a NaN stays as it is.
       int e = top >= 0x7f80u ? 0 : static_cast<int>(top >> 7) - 127 - 14;
       e = e < -100 ? -100 : e;
       const float down = __int_as_float((127 - e) << 23);
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i)
-        *reinterpret_cast<uint4*>(to + (i / 8) * C::kRowSlab + (((i % 8) ^ (r & 7)) << 4)) = scaled_f16(x[i], down);
+#pragma unroll 2
+      for (int i = 0; i < CR; ++i) {
+        uint4* x = reinterpret_cast<uint4*>(chunk(lane, i));
+        *x = scaled_f16(*x, down);
+      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full(slot));
@@ -962,7 +980,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
         const float unit = mt == -INFINITY ? 1.0f : ex2_ftz(mt - ms);
         const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
         char* orow = P.o + g.b * P.ob + row.head * P.oh + row.n * P.on;
-        const long long part_row = (2ll * blockIdx.x + (g.first ? 0 : 1)) * kRows + slot * 128 + r;
+        const long long part = 2ll * blockIdx.x + (g.first ? 0 : 1);
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
           uint32_t o32[32];
@@ -988,14 +1006,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                   make_uint4(pack_bf16x2(v[e] * inv, v[e + 1] * inv), pack_bf16x2(v[e + 2] * inv, v[e + 3] * inv),
                              pack_bf16x2(v[e + 4] * inv, v[e + 5] * inv), pack_bf16x2(v[e + 6] * inv, v[e + 7] * inv));
           } else if (row.valid) {
-            float4* to = reinterpret_cast<float4*>(P.part_o + part_row * D + c0);
+            // [part][channel][row]: a warp's rows side by side.
+            float* to = P.part_o + (part * D + c0) * kRows + slot * 128 + r;
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) to[e / 4] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+            for (int e = 0; e < 32; ++e) to[e * kRows] = v[e];
           }
         }
         if (row.valid && whole && P.lse != nullptr)
           P.lse[(static_cast<long long>(g.b) * P.Hq + row.head) * P.N + row.n] = (ms + log2f(l)) * 0.6931471805599453f;
-        if (row.valid && !whole) P.part_ml[part_row] = make_float2(ms, l);
+        if (row.valid && !whole) P.part_ml[part * kRows + slot * 128 + r] = make_float2(ms, l);
         tc_fence_before();
       } else {
         // No rows in this item: its slot's Q buffer is idle.
@@ -1020,56 +1039,57 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
 }
 
 // Merges the parts of the items that more than one CTA worked on: CTA (item,
-// 32 rows), a warp per row.
+// 32 rows), a row per lane and an eighth of the channels per warp.
 template <int D>
 __global__ void __launch_bounds__(256) cache_tc_merge_kernel(const __grid_constant__ TcParams T, int grid) {
   const CacheAttnParams& P = T.a;
   const int item = blockIdx.x / (kRows / 32), chunk = blockIdx.x % (kRows / 32);
   const int tile = item % P.tiles, bh = item / P.tiles;
   const int b = bh / P.c.H, h = bh % P.c.H;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int* pre = T.tile_prefix + static_cast<long long>(b) * (P.tiles + 1);
-  const int n = __ldg(pre + tile + 1) - __ldg(pre + tile);
+  const int n = pre[tile + 1] - pre[tile];
   if (n == 0) return;
-  const long long total = __ldg(T.seq_prefix + P.c.B);
+  const long long total = T.seq_prefix[P.c.B];
   const long long ctas = work_ctas(total, grid);
-  const long long w0 = __ldg(T.seq_prefix + b) + static_cast<long long>(h) * __ldg(pre + P.tiles) + __ldg(pre + tile);
+  const long long w0 = T.seq_prefix[b] + static_cast<long long>(h) * pre[P.tiles] + pre[tile];
   // CTA c holds tiles [total c / ctas, total (c + 1) / ctas).
   const int c0 = static_cast<int>(((w0 + 1) * ctas + total - 1) / total) - 1;
   const int c1 = static_cast<int>(((w0 + n) * ctas + total - 1) / total) - 1;
   if (c0 == c1) return;
   bool bad = false;
   const SeqInfo s = seq_info(P, b, &bad);
-  const int lane = threadIdx.x % 32;
-  constexpr int C = D / 32;
+  const int r = chunk * 32 + threadIdx.x % 32;
+  const CacheRow row = cache_row(P, tile * kRows + r, h, s.len, s.count);
+  if (!row.valid) return;
+  constexpr int C = D / 8;
+  const int ch = threadIdx.x / 32 * C;
   // The item is the first part of every CTA but, perhaps, its first one's.
   const int first_part = total * c0 / ctas >= w0 ? 0 : 1;
-  for (int i = threadIdx.x / 32; i < 32; i += 8) {
-    const int r = chunk * 32 + i;
-    const CacheRow row = cache_row(P, tile * kRows + r, h, s.len, s.count);
-    if (!row.valid) continue;
-    float m = -INFINITY;
-    for (int c = c0; c <= c1; ++c)
-      m = fmaxf(m, P.part_ml[(2ll * c + (c == c0 ? first_part : 0)) * kRows + r].x);
-    float l = 0.0f, acc[C] = {};
+  auto part_of = [&](int c) { return 2ll * c + (c == c0 ? first_part : 0); };
+  float m = -INFINITY;
 #pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-      const long long at = (2ll * c + (c == c0 ? first_part : 0)) * kRows + r;
-      const float2 p = P.part_ml[at];
-      // A part that saw no key has a sum of 0 (and an O of 0).
-      const float f = p.y == 0.0f ? 0.0f : (p.x == -INFINITY ? 1.0f : ex2_ftz(p.x - m));
-      l = fmaf(p.y, f, l);
-      const float* from = P.part_o + at * D + lane * C;
+  for (int c = c0; c <= c1; ++c) m = fmaxf(m, P.part_ml[part_of(c) * kRows + r].x);
+  float l = 0.0f, acc[C] = {};
+#pragma unroll 2
+  for (int c = c0; c <= c1; ++c) {
+    const float2 p = P.part_ml[part_of(c) * kRows + r];
+    // A part that saw no key has a sum of 0 (and an O of 0).
+    const float f = p.y == 0.0f ? 0.0f : (p.x == -INFINITY ? 1.0f : ex2_ftz(p.x - m));
+    l = fmaf(p.y, f, l);
+    const float* from = P.part_o + (part_of(c) * D + ch) * kRows + r;
 #pragma unroll
-      for (int e = 0; e < C; ++e) acc[e] = fmaf(from[e], f, acc[e]);
-    }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    char* to = P.o + b * P.ob + row.head * P.oh + row.n * P.on + 2 * lane * C;
-#pragma unroll
-    for (int e = 0; e < C; e += 2)
-      *reinterpret_cast<uint32_t*>(to + 2 * e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-    if (lane == 0 && P.lse != nullptr)
-      P.lse[(static_cast<long long>(b) * P.Hq + row.head) * P.N + row.n] = (m + log2f(l)) * 0.6931471805599453f;
+    for (int e = 0; e < C; ++e) acc[e] = fmaf(from[e * kRows], f, acc[e]);
   }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  char* to = P.o + b * P.ob + row.head * P.oh + row.n * P.on + 2 * ch;
+#pragma unroll
+  for (int e = 0; e < C; e += 8)
+    *reinterpret_cast<uint4*>(to + 2 * e) =
+        make_uint4(pack_bf16x2(acc[e] * inv, acc[e + 1] * inv), pack_bf16x2(acc[e + 2] * inv, acc[e + 3] * inv),
+                   pack_bf16x2(acc[e + 4] * inv, acc[e + 5] * inv), pack_bf16x2(acc[e + 6] * inv, acc[e + 7] * inv));
+  if (ch == 0 && P.lse != nullptr)
+    P.lse[(static_cast<long long>(b) * P.Hq + row.head) * P.N + row.n] = (m + log2f(l)) * 0.6931471805599453f;
 }
 
 struct Layout {
@@ -1100,10 +1120,25 @@ cudaError_t launch_d(const Ctx& c, const TcParams& T) {
   const cudaError_t e = cudaFuncSetAttribute(cache_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, CT<D>::kSmem);
   if (e != cudaSuccess) return e;
   cache_plan_kernel<<<1, 1024, 0, c.stream>>>(T);
-  cache_tc_kernel<D><<<c.num_sms, kThreads, CT<D>::kSmem, c.stream>>>(T);
+  // Each launched while the one before it runs; they wait for its end before
+  // they read what it wrote.
+  cudaLaunchAttribute early = {};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(c.num_sms);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = CT<D>::kSmem;
+  cfg.stream = c.stream;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  const cudaError_t ran = cudaLaunchKernelEx(&cfg, cache_tc_kernel<D>, T);
+  if (ran != cudaSuccess) return ran;
   const long long items = static_cast<long long>(T.a.c.B) * T.a.c.H * T.a.tiles;
-  cache_tc_merge_kernel<D><<<static_cast<unsigned>(items * (kRows / 32)), 256, 0, c.stream>>>(T, c.num_sms);
-  return cudaGetLastError();
+  cfg.gridDim = dim3(static_cast<unsigned>(items * (kRows / 32)));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, cache_tc_merge_kernel<D>, T, c.num_sms);
 }
 
 }  // namespace
