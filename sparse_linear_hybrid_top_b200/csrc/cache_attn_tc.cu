@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
   unsigned char* ring = qbuf + 2 * C::kOperand;             // [NS][d-slab][128 rows]
   unsigned char* raws = ring + NS * C::kOperand;            // [NR][128 keys][d codes]
   uint64_t* bars = reinterpret_cast<uint64_t*>(raws + NR * C::kRaw);
-  // full[NS] empty[NS] raw_full[NR] raw_empty[NR] q_full[2] q_free[2] s_full[2] p_half[2] p_full[2] o_done[2] drain[2] turn[8]
+  // full[NS] empty[NS] raw_full[NR] raw_empty[NR] q_full[2] q_free[2] s_full[2] p_half[2] p_full[2] o_done[2] drain[2] turn[8] open_max
   auto bar = [&](int i) { return smem_u32(bars + i); };
   auto full = [&](int i) { return bar(i); };
   auto empty = [&](int i) { return bar(NS + i); };
@@ -358,14 +358,18 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
   auto o_done = [&](int i) { return bar(B0 + 10 + i); };
   auto drain = [&](int i) { return bar(B0 + 12 + i); };
   auto turn = [&](int w) { return bar(B0 + 14 + w); };      // of softmax warp w
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + B0 + 22);
+  const uint32_t open_max = bar(B0 + 22);                   // the converting warps have their part of the open block
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + B0 + 23);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   // odd_seg[i % 8] = i + 1: part i's open block holds a value that is not finite.
   volatile int* odd_seg = abort_flag + 1;
-  static_assert((B0 + 22) * 8 + 4 + 4 + 32 <= C::kBarBytes, "barrier region");
+  // Largest magnitudes of the open block's finite keys and values (bf16 bits, two
+  // to a word), of each converting warp; two open blocks in turn.
+  uint32_t* open_tops = reinterpret_cast<uint32_t*>(const_cast<int*>(odd_seg) + 8);
+  static_assert((B0 + 23) * 8 + 4 + 4 + 32 + 32 <= C::kBarBytes, "barrier region");
   // Scales of tile i's two blocks in entry i % 8: of the keys (0: no page, its
-  // keys do not count), then of the values.  Warp 13 writes them with the bulk
-  // copy of the tile's keys: kRaws operand tiles before these are converted,
+  // keys do not count), then of the values.  Warp 13 writes them (the open
+  // block's: warp 8, with its keys) with the bulk copy of the tile's keys: kRaws operand tiles before these are converted,
   // and kStages before the MMAs of what they replace, so at most five tiles
   // before the softmax reads them.
   float4* scales = reinterpret_cast<float4*>(reinterpret_cast<unsigned char*>(bars) + C::kBarBytes);
@@ -397,6 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
     }
     for (int i = 0; i < 2; ++i) mbar_init(drain(i), 1);
     for (int i = 0; i < 8; ++i) mbar_init(turn(i), 1);
+    mbar_init(open_max, 4);
     *abort_flag = 0;
     for (int i = 0; i < 8; ++i) odd_seg[i] = 0;
     fence_mbar_init();
@@ -529,23 +534,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
         }
         return k;
       };
-      // Scale of the open block's finite keys or values.
-      auto open_scale = [&](const Seg& g, const void* base) {
-        const uint4* tail = reinterpret_cast<const uint4*>(
-            static_cast<const __nv_bfloat16*>(base) +
-            ((static_cast<long long>(g.b) * 2 + g.s.slot) * P.c.H + g.h) * kCacheBlock * D);
-        const int n = g.s.len % kCacheBlock * (D / 8);
-        uint32_t top = 0;
-#pragma unroll 8
-        for (int e = lane; e < n; e += 32) {
-          const uint4 x = __ldg(tail + e);
-          top = __vmaxu2(top, finite_or_zero(x.x) & 0x7fff7fffu);
-          top = __vmaxu2(top, finite_or_zero(x.y) & 0x7fff7fffu);
-          top = __vmaxu2(top, finite_or_zero(x.z) & 0x7fff7fffu);
-          top = __vmaxu2(top, finite_or_zero(x.w) & 0x7fff7fffu);
-        }
-        return tail_scale(__reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16)));
-      };
       unsigned long long at = 0;                  // operand tiles so far
       uint32_t tile_no = 0;                       // key tiles so far
       int part_no = 0;
@@ -560,15 +548,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
             cur = nxt;
             nxt = blocks_at(g, 2 * j + 32);
           }
-          float4 sc = make_float4(__shfl_sync(0xffffffffu, cur.ks, 2 * i), __shfl_sync(0xffffffffu, cur.ks, 2 * i + 1),
+          const float4 sc = make_float4(__shfl_sync(0xffffffffu, cur.ks, 2 * i), __shfl_sync(0xffffffffu, cur.ks, 2 * i + 1),
                                   __shfl_sync(0xffffffffu, cur.vs, 2 * i), __shfl_sync(0xffffffffu, cur.vs, 2 * i + 1));
           const int p0 = __shfl_sync(0xffffffffu, cur.page, 2 * i), p1 = __shfl_sync(0xffffffffu, cur.page, 2 * i + 1);
-          const int open = g.s.len / kCacheBlock - 2 * j;
-          if (open == 0 || open == 1) {
-            const float ks = open_scale(g, P.c.k_tail), vs = open_scale(g, P.c.v_tail);
-            (open ? sc.y : sc.x) = ks;
-            (open ? sc.w : sc.z) = vs;
-          }
 #pragma unroll 1
           for (int value = 0; value < 2 && ok; ++value, ++at) {
             const int rs = static_cast<int>(at % NR);
@@ -620,6 +602,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
     uint32_t tile_no = 0;
     int st = 0, rs = 0;
     uint32_t sph = 1, rph = 0;                  // parities of empty (first turn passes) and raw_full
+    uint32_t opens = 0;                         // open blocks so far
+    float open_vs = 1.0f;                       // the values' scale of the last one
     while (g.left > 0 && ok) {
 #pragma unroll 1
       for (int o = 2 * g.t0; o < 2 * g.t1 && ok; ++o) {
@@ -653,30 +637,79 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
           // The open block's rows, scaled, and zeros elsewhere.  Values that
           // are not finite would spread as 0 * inf; they are left to the rows
           // that see them.
-          const float inv = pow2_inv(value ? (closed == 1 ? sc.w : sc.z) : (closed == 1 ? sc.y : sc.x));
-          const uint4* tail = reinterpret_cast<const uint4*>(
-              static_cast<const __nv_bfloat16*>(value ? P.c.v_tail : P.c.k_tail) +
-              ((static_cast<long long>(g.b) * 2 + g.s.slot) * P.c.H + g.h) * kCacheBlock * D);
           const int open = closed == 0 || closed == 1 ? 64 * closed : 128;   // the open block's first row
           const int held = g.s.len % kCacheBlock;
-          bool odd = false;
 #pragma unroll 1
           for (int e = w * 32 + lane; e < 128 * (D / 8); e += 128) {
             const int row = e / (D / 8), ch = e % (D / 8);
-            if (row >= first && row < last) continue;
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (row >= open && row - open < held) {
-              x = __ldg(tail + (row - open) * (D / 8) + ch);
-              if (value) {
-                const uint4 y = make_uint4(finite_or_zero(x.x), finite_or_zero(x.y), finite_or_zero(x.z), finite_or_zero(x.w));
-                odd = odd || y.x != x.x || y.y != x.y || y.z != x.z || y.w != x.w;
-                x = y;
-              }
-              x = scaled_f16(x, inv);
-            }
-            *reinterpret_cast<uint4*>(dst + (ch / 8) * C::kRowSlab + row * 128 + (((ch % 8) ^ (row & 7)) << 4)) = x;
+            if ((row >= first && row < last) || (row >= open && row < open + 64)) continue;
+            *reinterpret_cast<uint4*>(dst + (ch / 8) * C::kRowSlab + row * 128 + (((ch % 8) ^ (row & 7)) << 4)) =
+                make_uint4(0u, 0u, 0u, 0u);
           }
-          if (odd) odd_seg[part_no % 8] = part_no + 1;
+          if (open < 128) {
+            // The block's loads are all in flight at once; with the keys the
+            // values too, whose scale the softmax wants then.
+            constexpr int E = D / 16;
+            const long long at = ((static_cast<long long>(g.b) * 2 + g.s.slot) * P.c.H + g.h) * kCacheBlock * D;
+            auto load = [&](const void* base, uint4 (&x)[E]) {
+              const uint4* tail = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + at);
+#pragma unroll
+              for (int i = 0; i < E; ++i) {
+                const int e = w * 32 + lane + 128 * i;
+                x[i] = e < held * (D / 8) ? __ldg(tail + e) : make_uint4(0u, 0u, 0u, 0u);
+              }
+            };
+            auto top_of = [&](const uint4 (&x)[E]) {
+              uint32_t top = 0;
+#pragma unroll
+              for (int i = 0; i < E; ++i) {
+                top = __vmaxu2(__vmaxu2(top, finite_or_zero(x[i].x) & 0x7fff7fffu), finite_or_zero(x[i].y) & 0x7fff7fffu);
+                top = __vmaxu2(__vmaxu2(top, finite_or_zero(x[i].z) & 0x7fff7fffu), finite_or_zero(x[i].w) & 0x7fff7fffu);
+              }
+              return __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+            };
+            uint4 x[E];
+            load(value ? P.c.v_tail : P.c.k_tail, x);
+            float scale = open_vs;
+            if (!value) {
+              uint4 y[E];
+              load(P.c.v_tail, y);
+              const uint32_t tops = top_of(x) | (top_of(y) << 16);
+              uint32_t* at_tops = open_tops + 4 * (opens & 1);
+              if (lane == 0) {
+                at_tops[w] = tops;
+                mbar_arrive(open_max);
+              }
+              if (!__all_sync(0xffffffffu, mbar_wait_poll(open_max, opens & 1u, wait_ns, abort_flag))) {
+                ok = false;
+                break;
+              }
+              ++opens;
+              const uint32_t all = __vmaxu2(__vmaxu2(at_tops[0], at_tops[1]), __vmaxu2(at_tops[2], at_tops[3]));
+              scale = tail_scale(all & 0xffffu);
+              open_vs = tail_scale(all >> 16);
+              if (w == 0 && lane == 0) {
+                float* to = reinterpret_cast<float*>(scales + tile_no % 8) + closed;
+                to[0] = scale;
+                to[2] = open_vs;
+              }
+            }
+            const float inv = pow2_inv(scale);
+            bool odd = false;
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+              const int e = w * 32 + lane + 128 * i, row = open + e / (D / 8), ch = e % (D / 8);
+              if (value) {
+                const uint4 y = make_uint4(finite_or_zero(x[i].x), finite_or_zero(x[i].y), finite_or_zero(x[i].z),
+                                           finite_or_zero(x[i].w));
+                odd = odd || y.x != x[i].x || y.y != x[i].y || y.z != x[i].z || y.w != x[i].w;
+                x[i] = y;
+              }
+              *reinterpret_cast<uint4*>(dst + (ch / 8) * C::kRowSlab + row * 128 + (((ch % 8) ^ (row & 7)) << 4)) =
+                  scaled_f16(x[i], inv);
+            }
+            if (odd) odd_seg[part_no % 8] = part_no + 1;
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
