@@ -854,13 +854,23 @@ cudaError_t launch_d(const Ctx& c, const CacheAttnParams& P, const Shape& s) {
 
 }  // namespace
 
-// Rows of a (sequence, key head) from which the tensor-core kernel takes over.
-static bool many_rows(const CacheAttnArgs& a) {
-  return static_cast<long long>(a.Hq / a.cache.H) * a.N > 64;
+// Whether the tensor-core kernel takes the call: with more than 64 rows of a
+// (sequence, key head), which is what a CTA of this file's kernel holds, and
+// with more than 32 where the tables have room for much work.  At 33 to 64 rows
+// this kernel takes some 0.95 us and that one 0.7 us for each half page of an
+// SM, and that one 20 us more to begin and end (64 rows and 12 heads: 36 us here
+// and 45 there for 7800 keys, 81 and 81 for 31200; 60 rows, 8 heads and 16
+// sequences of 8640 keys: 234 and 154).  Lengths are not known here; a table
+// much wider than its sequences costs the difference of the short ones.  At 17
+// to 32 rows this one is ahead at any length (31200 keys: 49 and 86).
+static bool many_rows(const CacheAttnArgs& a, int num_sms) {
+  const long long rows = static_cast<long long>(a.Hq / a.cache.H) * a.N;
+  const long long blocks = static_cast<long long>(a.cache.B) * a.cache.H * a.cache.blocks;
+  return rows > 64 || (rows > 32 && blocks > 40ll * num_sms);
 }
 
 size_t cache_attn_ws_bytes(const CacheAttnArgs& a, int num_sms) {
-  if (many_rows(a)) return cache_attn_tc_ws_bytes(a, num_sms);
+  if (many_rows(a, num_sms)) return cache_attn_tc_ws_bytes(a, num_sms);
   return shape_of(a, num_sms).total;
 }
 
@@ -885,7 +895,7 @@ cudaError_t launch_cache_attn(const Ctx& c, const CacheAttnArgs& a) {
   P.part_o = nullptr;
   P.part_ml = nullptr;
   P.plan = nullptr;
-  if (many_rows(a)) return launch_cache_attn_tc(c, a, P);
+  if (many_rows(a, c.num_sms)) return launch_cache_attn_tc(c, a, P);
   const Shape s = shape_of(a, c.num_sms);
   P.tiles = 1;
   if (s.merge) {

@@ -526,3 +526,14 @@ def test_calls_at_the_same_time_on_two_streams(N):
     for i in range(2):
         for o in got[i]:
             assert torch.equal(o, want[i])       # the split does not depend on timing
+
+
+@needs_gpu
+@pytest.mark.parametrize("N,Hq", [(33, 2), (64, 2), (11, 10)])
+def test_rows_at_the_border_of_two_kernels(N, Hq):
+    """33 to 64 rows of a key head: another kernel where the tables have room for
+    much work."""
+    for blocks in (20, 1600):
+        cache, seq = _make(2, 2, 64, [700, 1200], blocks=blocks, seed=blocks)
+        _check(cache, _q(2, Hq, N, 64, N), seq, frame=1)
+        _check(cache, _q(2, Hq, N, 64, N), seq, [N, 5], window=100)
