@@ -9,6 +9,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "operators.h"
 #include "salad.h"
 
 namespace salad {

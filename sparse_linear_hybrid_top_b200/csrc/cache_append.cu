@@ -25,7 +25,7 @@
 
 #include "cache_index.h"
 #include "common.cuh"
-#include "internal.h"
+#include "operators.h"
 
 namespace salad {
 namespace {

@@ -17,7 +17,6 @@ namespace salad {
 // Device error bits, OR-ed into the library's error word.
 constexpr unsigned kErrTimeout = 1u;   // a bounded wait ran out
 constexpr unsigned kErrLayout = 2u;    // a kernel found its shared memory misaligned
-constexpr unsigned kErrRange = 4u;     // a cache operator skipped a page, length or count out of range
 
 // ------------------------------------------------------------------ misc --
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -84,46 +83,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
     if (mbar_try_wait(bar, parity)) return true;
     if (abort != nullptr && *abort) return false;
     if (globaltimer_ns() - t0 > limit_ns) return false;
-  }
-}
-
-// The same with the timer read every 64 polls only: reading it costs hundreds
-// of cycles, which a wait inside a short dependency chain feels.
-__device__ __forceinline__ bool mbar_wait_poll(uint32_t bar, uint32_t parity, uint64_t limit_ns,
-                                               volatile int* abort) {
-  uint64_t t0 = 0;
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (abort != nullptr && *abort) return false;
-    if ((i & 63u) == 0) {
-      const uint64_t now = globaltimer_ns();
-      if (t0 == 0) t0 = now;
-      else if (now - t0 > limit_ns) return false;
-    }
-  }
-}
-
-// The same without suspending between polls: for one thread whose wake-up
-// is on the critical path.
-__device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity, uint64_t limit_ns,
-                                               volatile int* abort) {
-  uint64_t t0 = 0;
-  for (uint32_t i = 1;; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if ((i & 255u) == 0) {
-      if (abort != nullptr && *abort) return false;
-      const uint64_t now = globaltimer_ns();
-      if (t0 == 0) t0 = now;
-      else if (now - t0 > limit_ns) return false;
-    }
   }
 }
 
@@ -240,11 +199,6 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn_major,
          | (1u << 10)                                // B bf16
          | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
-}
-
-// The same with fp16 A and B.
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn_major, bool b_mn_major) {
-  return idesc_bf16(M, N, a_mn_major, b_mn_major) & ~((1u << 7) | (1u << 10));
 }
 
 // ---- TMEM loads/stores: 32 lanes x 32 bits, 32 consecutive columns, with the

@@ -24,7 +24,7 @@
 #include <cuda_fp16.h>
 
 #include "common.cuh"
-#include "internal.h"
+#include "operators.h"
 #include "rope.cuh"
 
 namespace salad {
