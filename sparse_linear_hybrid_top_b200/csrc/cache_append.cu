@@ -279,18 +279,27 @@ cudaError_t launch_cache_append(const Ctx& c, const CacheAppendArgs& a) {
   if (a.rotate) P.rates = rope_rates(a.split, a.base);
   else P.rates = RopeRates{};
   P.err = c.err;
-  // Blocks that N tokens can touch.  Heads share a CTA (and its cosines) as
-  // far as the CTAs still fill two places on every SM, and eight at most, so
-  // that CTAs behind a padded batch's counts, which end at once, do not leave
-  // others a second turn (4 x 40 heads x 3600 padded tokens: 74 us with four
-  // heads to a CTA, 66 with eight, 72 with twelve).
+  // Blocks that N tokens can touch.
   const int span = (a.N + kCacheBlock - 1) / kCacheBlock + 1;
-  const long long units = static_cast<long long>(span) * a.cache.B * a.cache.H;
-  long long per = units / (2ll * c.num_sms);
-  if (per > 8) per = 8;
-  if (per < 1) per = 1;
-  if (per > a.cache.H) per = a.cache.H;
-  P.heads_per_cta = static_cast<int>(per);
+  // Heads of a CTA, which share its angles: up to eight (so that CTAs behind a
+  // padded batch's counts, which end at once, do not leave others a second turn:
+  // 4 x 40 heads x 3600 padded tokens take 66 us with eight and 72 with
+  // twelve), as many as cost least where a CTA takes 1.5 heads' time to begin,
+  // two are on an SM, and the last ones leave half a turn unused (7800 tokens of
+  // 12 heads: 21.4 us in 3 groups, a turn and a quarter, 18.3 in 2; 512
+  // tokens of 8 heads, 16 sequences: 18.3 in 3, 14.2 in 2).
+  const double touched = ((a.N - 1) / static_cast<double>(kCacheBlock) + 1.0) * a.cache.B;
+  int per = 1;
+  double least = 0.0;
+  for (int n = 1; n <= 8 && n <= a.cache.H; ++n) {
+    const double turns = touched * ((a.cache.H + n - 1) / n) / (2.0 * c.num_sms);
+    const double cost = (turns <= 1.02 ? 1.0 : turns + 0.5) * (n + 1.5);
+    if (n == 1 || cost < least) {
+      per = n;
+      least = cost;
+    }
+  }
+  P.heads_per_cta = per;
   const dim3 grid(span, static_cast<unsigned>((a.cache.H + per - 1) / per), a.cache.B);
   const bool halves = a.pairing == 1;
   if (a.cache.d == 128) {
