@@ -40,8 +40,8 @@
 //
 // Measured (d = 128): one token, 12 heads, 31200 keys 29.8 us, 124800 keys 73.6
 // us (5.2 TB/s; 14 us are launches, the chain lengths - table - pages - rows, and
-// the merge); 16 tokens on 31200 keys 30.7 us, 32 49 us, 64 82 us, where the
-// converting and exponentials of one more 16-row tile cost more than the memory;
+// the merge); 16 tokens on 31200 keys 30.7 us, 32 49 us, where the second tile's
+// products and exponentials take longer than the memory;
 // 16 unequal sequences of 40 heads on 8 65.5 us (4.4 TB/s).
 #include "cache_attn.cuh"
 
@@ -863,16 +863,15 @@ cudaError_t launch_d(const Ctx& c, const CacheAttnParams& P, const Shape& s) {
 // Whether the tensor-core kernel takes the call: with more than 64 rows of a
 // (sequence, key head), which is what a CTA of this file's kernel holds, and
 // with more than 32 where the tables have room for much work.  At 33 to 64 rows
-// this kernel takes some 0.95 us and that one 0.7 us for each half page of an
-// SM, and that one 20 us more to begin and end (64 rows and 12 heads: 36 us here
-// and 45 there for 7800 keys, 81 and 81 for 31200; 60 rows, 8 heads and 16
-// sequences of 8640 keys: 234 and 154).  Lengths are not known here; a table
-// much wider than its sequences costs the difference of the short ones.  At 17
-// to 32 rows this one is ahead at any length (31200 keys: 49 and 86).
+// (64 here, 65 there; 12 heads) 1000 keys take 25 us and 27, 7800 36 and 38,
+// 31200 82 and 75; 60 rows, 8 heads and 16 sequences of 8640 keys 234 and 154.
+// Lengths are not known here; a table much wider than its sequences costs the
+// difference of the short ones.  At 17 to 32 rows this one is ahead at any
+// length (31200 keys: 49 and 75).
 static bool many_rows(const CacheAttnArgs& a, int num_sms) {
   const long long rows = static_cast<long long>(a.Hq / a.cache.H) * a.N;
   const long long blocks = static_cast<long long>(a.cache.B) * a.cache.H * a.cache.blocks;
-  return rows > 64 || (rows > 32 && blocks > 40ll * num_sms);
+  return rows > 64 || (rows > 32 && blocks > 16ll * num_sms);
 }
 
 size_t cache_attn_ws_bytes(const CacheAttnArgs& a, int num_sms) {

@@ -47,7 +47,8 @@
 // frame.  A first launch sums the items' tiles; every CTA then takes an equal
 // run of tiles, which may begin and end inside an item.  An item that one CTA
 // holds whole is written at once; the others leave float32 parts (two per
-// CTA at most), merged by a last launch.
+// CTA at most), merged by a last launch.  Every CTA notes the item that its run
+// begins inside, so that the merge looks at those alone.
 #include <cstring>
 
 #include "cache_attn.cuh"
@@ -85,10 +86,17 @@ struct CT {
   static constexpr uint32_t kCols = 512;
 };
 
+// The item that a CTA's run begins inside (tile < 0: it begins with one).
+struct Inside {
+  long long start;            // the item's first tile, of all
+  int b, h, tile, n;          // n: its tiles
+};
+
 struct TcParams {
   CacheAttnParams a;          // tiles: items of a (sequence, key head)
   int* tile_prefix;           // [B][tiles + 1]
   long long* seq_prefix;      // [B + 1], tiles of all heads of the sequences before
+  Inside* inside;             // [CTAs]
 };
 
 // Tiles of keys that item `tile` of a sequence walks over: [first, first + n).
@@ -612,6 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
     Seg g = seg_at(T, w0, w1 - w0);
     int part_no = 0;
     uint32_t tile_no = 0;
+    if (w == 0 && lane == 0) T.inside[blockIdx.x] = Inside{w0 - g.t0, g.b, g.h, g.t0 > 0 ? g.tile : -1, g.all.n};
     int st = 0, rs = 0;
     uint32_t sph = 1, rph = 0;                  // parities of empty (first turn passes) and raw_full
     uint32_t opens = 0;                         // open blocks so far
@@ -1083,63 +1092,104 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
   }
 }
 
-// Merges the parts of the items that more than one CTA worked on: CTA (item,
-// 32 rows), a row per lane and an eighth of the channels per warp.
+// Merges the parts of the items that more than one CTA worked on: a CTA for
+// each CTA whose run begins inside an item, and 32 rows; a row per lane.  An
+// item of n parts has n - 1 such CTAs.  The first S of them (8, 4 or, with up
+// to four parts, 1) take a slice of the channels each; a warp has an eighth of
+// the channels and every S-th part.  (With the parts one after the other 147 rows of 2 sequences
+// on 20000 and 11000 keys, d = 64, 79 and 44 parts, took 97 us in all: 35 this
+// way; few parts leave from the registers, since the exchange took 10 us of
+// issue where every SM has eight such CTAs.)
 template <int D>
 __global__ void __launch_bounds__(256) cache_tc_merge_kernel(const __grid_constant__ TcParams T, int grid) {
   const CacheAttnParams& P = T.a;
-  const int item = blockIdx.x / (kRows / 32), chunk = blockIdx.x % (kRows / 32);
-  const int tile = item % P.tiles, bh = item / P.tiles;
-  const int b = bh / P.c.H, h = bh % P.c.H;
+  constexpr int C = D / 8, PAD = 33;
+  __shared__ float os[8][C][PAD];
+  __shared__ float2 mls[8][32];
+  const int cta = blockIdx.x / (kRows / 32), r0 = blockIdx.x % (kRows / 32) * 32;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int* pre = T.tile_prefix + static_cast<long long>(b) * (P.tiles + 1);
-  const int n = pre[tile + 1] - pre[tile];
-  if (n == 0) return;
   const long long total = T.seq_prefix[P.c.B];
   const long long ctas = work_ctas(total, grid);
-  const long long w0 = T.seq_prefix[b] + static_cast<long long>(h) * pre[P.tiles] + pre[tile];
+  const Inside in = T.inside[cta];
+  if (cta == 0 || cta >= ctas) return;
+  // (Beyond `tile < 0`: a launch that refused to run has noted nothing.)
+  if (in.tile < 0 || in.tile >= P.tiles || in.b < 0 || in.b >= P.c.B || in.h < 0 || in.h >= P.c.H || in.n < 1 ||
+      in.start < 0 || in.start + in.n > total)
+    return;
   // CTA c holds tiles [total c / ctas, total (c + 1) / ctas).
-  const int c0 = static_cast<int>(((w0 + 1) * ctas + total - 1) / total) - 1;
-  const int c1 = static_cast<int>(((w0 + n) * ctas + total - 1) / total) - 1;
-  if (c0 == c1) return;
+  const int c0 = static_cast<int>(((in.start + 1) * ctas + total - 1) / total) - 1;
+  const int c1 = static_cast<int>(((in.start + in.n) * ctas + total - 1) / total) - 1;
+  const int split = c1 - c0 >= 8 ? 8 : (c1 - c0 >= 4 ? 4 : 1);
+  const int slice = cta - c0 - 1;
+  if (slice >= split) return;
   bool bad = false;
-  const SeqInfo s = seq_info(P, b, &bad);
-  const int r = chunk * 32 + threadIdx.x % 32;
-  const CacheRow row = cache_row(P, tile * kRows + r, h, s.len, s.count);
-  if (!row.valid) return;
-  constexpr int C = D / 8;
-  const int ch = threadIdx.x / 32 * C;
+  const SeqInfo s = seq_info(P, in.b, &bad);
+  if (in.tile * kRows + r0 >= s.count * P.group) return;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int groups = 8 / split;        // of channels, in this CTA
+  const int ch0 = slice * groups * C, ch = ch0 + warp % groups * C, c_first = c0 + warp / groups;
   // The item is the first part of every CTA but, perhaps, its first one's.
-  const int first_part = total * c0 / ctas >= w0 ? 0 : 1;
+  const int first_part = total * c0 / ctas >= in.start ? 0 : 1;
   auto part_of = [&](int c) { return 2ll * c + (c == c0 ? first_part : 0); };
+  // A part that saw no key has a sum of 0 (and an O of 0).
+  auto weight = [](float2 p, float top) { return p.y == 0.0f ? 0.0f : (p.x == -INFINITY ? 1.0f : ex2_ftz(p.x - top)); };
   float m = -INFINITY;
 #pragma unroll 4
-  for (int c = c0; c <= c1; ++c) m = fmaxf(m, P.part_ml[part_of(c) * kRows + r].x);
+  for (int c = c_first; c <= c1; c += split) m = fmaxf(m, P.part_ml[part_of(c) * kRows + r0 + lane].x);
   float l = 0.0f, acc[C] = {};
 #pragma unroll 2
-  for (int c = c0; c <= c1; ++c) {
-    const float2 p = P.part_ml[part_of(c) * kRows + r];
-    // A part that saw no key has a sum of 0 (and an O of 0).
-    const float f = p.y == 0.0f ? 0.0f : (p.x == -INFINITY ? 1.0f : ex2_ftz(p.x - m));
+  for (int c = c_first; c <= c1; c += split) {
+    const float2 p = P.part_ml[part_of(c) * kRows + r0 + lane];
+    const float f = weight(p, m);
     l = fmaf(p.y, f, l);
-    const float* from = P.part_o + (part_of(c) * D + ch) * kRows + r;
+    const float* from = P.part_o + (part_of(c) * D + ch) * kRows + r0 + lane;
 #pragma unroll
     for (int e = 0; e < C; ++e) acc[e] = fmaf(from[e * kRows], f, acc[e]);
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  char* to = P.o + b * P.ob + row.head * P.oh + row.n * P.on + 2 * ch;
+  if (split == 1) {
+    // The row's sums are all here.
+    const CacheRow row = cache_row(P, in.tile * kRows + r0 + lane, in.h, s.len, s.count);
+    if (!row.valid) return;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    char* to = P.o + in.b * P.ob + row.head * P.oh + row.n * P.on + 2 * ch;
 #pragma unroll
-  for (int e = 0; e < C; e += 8)
-    *reinterpret_cast<uint4*>(to + 2 * e) =
-        make_uint4(pack_bf16x2(acc[e] * inv, acc[e + 1] * inv), pack_bf16x2(acc[e + 2] * inv, acc[e + 3] * inv),
-                   pack_bf16x2(acc[e + 4] * inv, acc[e + 5] * inv), pack_bf16x2(acc[e + 6] * inv, acc[e + 7] * inv));
-  if (ch == 0 && P.lse != nullptr)
-    P.lse[(static_cast<long long>(b) * P.Hq + row.head) * P.N + row.n] = (m + log2f(l)) * 0.6931471805599453f;
+    for (int e = 0; e < C; e += 8)
+      *reinterpret_cast<uint4*>(to + 2 * e) =
+          make_uint4(pack_bf16x2(acc[e] * inv, acc[e + 1] * inv), pack_bf16x2(acc[e + 2] * inv, acc[e + 3] * inv),
+                     pack_bf16x2(acc[e + 4] * inv, acc[e + 5] * inv), pack_bf16x2(acc[e + 6] * inv, acc[e + 7] * inv));
+    if (ch == 0 && P.lse != nullptr)
+      P.lse[(static_cast<long long>(in.b) * P.Hq + row.head) * P.N + row.n] = (m + log2f(l)) * 0.6931471805599453f;
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < C; ++e) os[warp][e][lane] = acc[e];
+  mls[warp][lane] = make_float2(m, l);
+  __syncthreads();
+  // Two channels of a row at a time, a row's side by side.
+  const int pairs = groups * C / 2, log_pairs = __ffs(pairs) - 1;
+  for (int x = threadIdx.x; x < 32 * pairs; x += 256) {
+    const int pair = x & (pairs - 1), i = x >> log_pairs, g = pair / (C / 2), e = pair % (C / 2) * 2;
+    const CacheRow row = cache_row(P, in.tile * kRows + r0 + i, in.h, s.len, s.count);
+    if (!row.valid) continue;
+    float top = -INFINITY, sum = 0.0f, a0 = 0.0f, a1 = 0.0f;
+    for (int k = g; k < 8; k += groups) top = fmaxf(top, mls[k][i].x);
+    for (int k = g; k < 8; k += groups) {
+      const float f = weight(mls[k][i], top);
+      sum = fmaf(mls[k][i].y, f, sum);
+      a0 = fmaf(os[k][e][i], f, a0);
+      a1 = fmaf(os[k][e + 1][i], f, a1);
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    *reinterpret_cast<uint32_t*>(P.o + in.b * P.ob + row.head * P.oh + row.n * P.on + 2 * (ch0 + g * C + e)) =
+        pack_bf16x2(a0 * inv, a1 * inv);
+    if (ch0 == 0 && pair == 0 && P.lse != nullptr)
+      P.lse[(static_cast<long long>(in.b) * P.Hq + row.head) * P.N + row.n] = (top + log2f(sum)) * 0.6931471805599453f;
+  }
 }
 
 struct Layout {
   int tiles;
-  size_t part_o, part_ml, tile_prefix, seq_prefix, total;
+  size_t part_o, part_ml, tile_prefix, seq_prefix, inside, total;
 };
 Layout layout_of(const CacheAttnArgs& a, int num_sms) {
   Layout L;
@@ -1156,6 +1206,7 @@ Layout layout_of(const CacheAttnArgs& a, int num_sms) {
   L.part_ml = take(parts * sizeof(float2));
   L.tile_prefix = take(static_cast<size_t>(a.cache.B) * (L.tiles + 1) * sizeof(int));
   L.seq_prefix = take((static_cast<size_t>(a.cache.B) + 1) * sizeof(long long));
+  L.inside = take(num_sms * sizeof(Inside));
   L.total = off;
   return L;
 }
@@ -1179,8 +1230,7 @@ cudaError_t launch_d(const Ctx& c, const TcParams& T) {
   cfg.numAttrs = 1;
   const cudaError_t ran = cudaLaunchKernelEx(&cfg, cache_tc_kernel<D>, T);
   if (ran != cudaSuccess) return ran;
-  const long long items = static_cast<long long>(T.a.c.B) * T.a.c.H * T.a.tiles;
-  cfg.gridDim = dim3(static_cast<unsigned>(items * (kRows / 32)));
+  cfg.gridDim = dim3(c.num_sms * (kRows / 32));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, cache_tc_merge_kernel<D>, T, c.num_sms);
@@ -1200,6 +1250,7 @@ cudaError_t launch_cache_attn_tc(const Ctx& c, const CacheAttnArgs& a, CacheAttn
   T.a = P;
   T.tile_prefix = reinterpret_cast<int*>(ws + L.tile_prefix);
   T.seq_prefix = reinterpret_cast<long long*>(ws + L.seq_prefix);
+  T.inside = reinterpret_cast<Inside*>(ws + L.inside);
   return a.cache.d == 128 ? launch_d<128>(c, T) : launch_d<64>(c, T);
 }
 
