@@ -35,14 +35,15 @@
 // CTA enters a further sequence: it has nothing in flight from the last one's
 // end to the next one's first page (40 heads on 8, 16 sequences of 1346 to 16001
 // keys: 73.5 us with 0, 63.3 with 8, 63.7 with 16, 64.2 with 32; 16 of 1196 to
-// 2111 keys and 12 heads 33.4, 31.5, 30.8, 33.9).  A sequence that one CTA holds whole is written at
-// once, the parts of the others are merged by a second launch.
+// 2111 keys and 12 heads 33.4, 31.5, 30.8, 33.9).  A sequence that one CTA holds
+// whole is written at once, the parts of the others are merged by a second
+// launch.
 //
 // Measured (d = 128): one token, 12 heads, 31200 keys 29.8 us, 124800 keys 73.6
 // us (5.2 TB/s; 14 us are launches, the chain lengths - table - pages - rows, and
 // the merge); 16 tokens on 31200 keys 30.7 us, 32 49 us, where the second tile's
-// products and exponentials take longer than the memory;
-// 16 unequal sequences of 40 heads on 8 65.5 us (4.4 TB/s).
+// products and exponentials take longer than the memory; 16 unequal sequences of
+// 40 heads on 8 65.5 us (4.4 TB/s).
 #include "cache_attn.cuh"
 
 namespace salad {

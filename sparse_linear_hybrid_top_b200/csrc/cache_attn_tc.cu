@@ -33,8 +33,8 @@
 // softmax runs.  P overwrites S in TMEM.
 //
 // Measured (d = 128): 4680 query tokens (three frames of 1560) on 23400 keys, 12
-// heads, 558 us; 3600 on 104400, 8 heads, 1.75 ms: 880 and 860 TFLOP/s, 0.53 and
-// 0.51 of the burst rate of a large matrix product.  A pair of tiles takes 1.75
+// heads, 558 us; 3600 on 104400, 8 heads, 1.72 ms: 880 and 860 TFLOP/s, 0.53 and
+// 0.52 of the burst rate of a large matrix product.  A pair of tiles takes 1.75
 // times its products' cycles.  No unit bounds it alone (timed with parts left
 // out: without the exponentials 0.85 of the time, without the conversion 0.9,
 // with an eighth of the products 0.83): the way of a slot, S - maximum -
