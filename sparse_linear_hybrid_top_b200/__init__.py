@@ -527,7 +527,8 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor] = None, *, positions=None, g
          offset: int = 0, base: float = 10000.0, split: Optional[Sequence[int]] = None,
          pairing: str = "adjacent", q_out=None, k_out=None, stream=None):
     """Rotary positions with up to three axes on q [B,Hq,N,d] and k [B,Hk,N,d]
-    (bf16, fp16 or fp32; contiguous rows, any other strides): y = R(pos) x.
+    (bf16, fp16 or fp32; contiguous rows, other strides multiples of 16
+    bytes): y = R(pos) x.
 
     positions: int32 [N,3] or [B,N,3]; or grid = (Hh, Wh), the frame-major
     latent whose token n stands at p = offset + n.  split: channels of the
@@ -619,12 +620,18 @@ def _cache_call(cache, seq, counts):
             0 if counts is None else _flat(counts, (cache.B,), torch.int32, dev, "counts"))
 
 
+def _no_grad(what: str, *tensors) -> None:
+    """Refuses a call whose gradient would be lost without a word."""
+    if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
+        raise ValueError(f"{what} has no backward pass: call it under torch.no_grad()")
+
+
 def cache_append(cache: BlockCache, k: torch.Tensor, v: torch.Tensor, seq: torch.Tensor, *,
                  counts=None, positions=None, grid=None, base: float = 10000.0,
                  split: Optional[Sequence[int]] = None, pairing: str = "adjacent", seq_out=None,
                  stream=None) -> torch.Tensor:
-    """Appends k, v (bf16 [B,H,N,d], contiguous rows, any other strides) to the
-    cache behind the tokens that ``seq`` says it holds, and returns seq_out,
+    """Appends k, v (bf16 [B,H,N,d], contiguous rows, other strides multiples
+    of 16 bytes) to the cache behind the tokens that ``seq`` says it holds, and returns seq_out,
     the state after it (``seq`` itself may be given: it is advanced in place).
 
     counts: int32 [B], valid tokens of each row of the batch (default all N).
@@ -639,6 +646,7 @@ def cache_append(cache: BlockCache, k: torch.Tensor, v: torch.Tensor, seq: torch
     N = k.shape[2]
     shape = (cache.B, cache.H, N, cache.d)
     k_st, v_st = _rows(k, shape, torch.bfloat16, dev, "k"), _rows(v, shape, torch.bfloat16, dev, "v")
+    _no_grad("salad_cache_append", k, v)
     rotate = positions is not None or grid is not None
     if rotate:
         split, pair, at, batched, Hh, Wh = _rotation(cache.d, split, pairing, positions, grid, cache.B, N, dev)
@@ -656,8 +664,8 @@ def cache_append(cache: BlockCache, k: torch.Tensor, v: torch.Tensor, seq: torch
 def cache_attn(cache: BlockCache, q: torch.Tensor, seq: torch.Tensor, *, counts=None, frame: int = 0,
                window: int = -1, scale: Optional[float] = None, o=None, lse=None, workspace=None,
                stream=None) -> torch.Tensor:
-    """Attention of q (bf16 [B,Hq,N,d], contiguous rows, any other strides),
-    the last tokens that ``seq`` says the cache holds, over the whole cache.
+    """Attention of q (bf16 [B,Hq,N,d], contiguous rows, other strides
+    multiples of 16 bytes), the last tokens that ``seq`` says the cache holds, over the whole cache.
 
     Hq is a multiple of the cache's heads.  counts: int32 [B], valid rows of
     each sample (default all N; the others are not written).  frame: 0, every
@@ -672,6 +680,7 @@ def cache_attn(cache: BlockCache, q: torch.Tensor, seq: torch.Tensor, *, counts=
     Hq, N = q.shape[1:3]
     shape = (cache.B, Hq, N, cache.d)
     q_st = _rows(q, shape, torch.bfloat16, dev, "q")
+    _no_grad("salad_cache_attn", q)
     if o is None:
         o = _empty_on(stream, lambda: torch.empty_like(q))
     o_st = _rows(o, shape, torch.bfloat16, dev, "o")

@@ -10,8 +10,8 @@ The one of many rows multiplies c_j = v_j / s_j, s_j the power-of-two scale of
 the key's block, by P_j = p_j s_j / max_i(p_i s_i), rounded to fp16: by 2^-11
 of it, or by half of fp16's smallest step, 2^-25, where that is more.  The
 latter adds at most F = 2^-25 max_i(p_i s_i) sum_j |c_j| / sum_j p_j.  The sums
-of weights and of products are float32 (n 2^-23 A each for n keys; n <= 2200
-here), and the output is rounded to bf16 (2^-8 |o|).  lse moves by D and
+of weights and of products are float32 (n 2^-23 A each for n keys: the longest
+sequence's), and the output is rounded to bf16 (2^-8 |o|).  lse moves by D and
 n 2^-23.
 """
 import ctypes
@@ -537,3 +537,40 @@ def test_rows_at_the_border_of_two_kernels(N, Hq):
         cache, seq = _make(2, 2, 64, [700, 1200], blocks=blocks, seed=blocks)
         _check(cache, _q(2, Hq, N, 64, N), seq, frame=1)
         _check(cache, _q(2, Hq, N, 64, N), seq, [N, 5], window=100)
+
+
+@needs_gpu
+def test_no_gradient_is_lost():
+    """Neither cache call has a backward pass: under grad mode it refuses inputs that ask for one."""
+    cache, seq = _make(1, 2, 64, [100])
+    x = torch.randn(1, 2, 3, 64, device="cuda", dtype=torch.bfloat16)
+    g = x.clone().requires_grad_()
+    for call in (lambda: salad.cache_attn(cache, g, seq), lambda: salad.cache_append(cache, g, x, seq),
+                 lambda: salad.cache_append(cache, x, g, seq)):
+        with pytest.raises(ValueError, match="backward"):
+            call()
+    with torch.no_grad():
+        assert torch.equal(salad.cache_attn(cache, g, seq), salad.cache_attn(cache, x, seq))
+
+
+@needs_gpu
+def test_pages_behind_four_gigabytes():
+    """A pool of more than 2^32 bytes, the sequence in its last pages: the same
+    bits as in a small pool, from the append and from both attention kernels."""
+    B, H, d, n = 1, 8, 128, 700
+    g = torch.Generator().manual_seed(2)
+    k, v = (torch.randn(B, H, n, d, generator=g).bfloat16().cuda() for _ in range(2))
+    small = salad.BlockCache.allocate(B, H, d, 11)
+    big = salad.BlockCache.allocate(B, H, d, 11, pages=68000)
+    assert big.k_pages.numel() > 1 << 32
+    big.page_table.copy_(67989 + torch.arange(11))
+    after = [salad.cache_append(c, k, v, c.new_seq(), grid=(4, 5)) for c in (small, big)]
+    assert torch.equal(after[0], after[1])
+    for name in ("k_pages", "v_pages"):
+        x, y = getattr(small, name).view(torch.uint8), getattr(big, name).view(torch.uint8)
+        assert torch.equal(x[:10], y[67989:67999])
+    assert torch.equal(small.k_scale[:10], big.k_scale[67989:67999])
+    for N in (1, 70):
+        q = _q(B, H, N, d, N)
+        assert torch.equal(salad.cache_attn(small, q, after[0], frame=1), salad.cache_attn(big, q, after[1], frame=1))
+    salad.check_error()
