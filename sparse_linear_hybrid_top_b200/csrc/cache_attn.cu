@@ -24,9 +24,11 @@
 // one instruction per pair.  Key scales, and the power of two that brings a
 // query row into fp16's range, join the softmax scale.  P carries the power of
 // two of its value block and is kept against the largest product of weight and
-// scale, the row sum against the largest weight.  The open block is multiplied
-// in bf16 as it is held.  P is rounded to fp16 (2^-11 of each weight) or bf16
-// (2^-8); maxima, sums and O are float32.
+// scale, the row sum against the largest weight.  P, at most 2^15, is rounded to
+// fp16: by 2^-11 of itself, or, 2^29 and more below the row's largest product of
+// weight and scale, by 2^-40 of that.  The open block is multiplied in bf16 as it
+// is held, by P rounded to bf16 (2^-8 of each weight).  Maxima, sums and O are
+// float32.
 //
 // Balance: lengths are known on the device only and differ in a batch.  Every
 // CTA sums them (up to 512 sequences) and takes an equal run of a head's work,
@@ -102,6 +104,10 @@ struct Ring {
   static constexpr int kSmem = kBytes + kBars;
 };
 
+// P of the open block, which is multiplied in bf16 by values of any size, is at
+// most 2^(kTopP - kOpenLift) = 2^-7: 64 products do not pass the largest value.
+// (The sums so far give way in float32: the open block comes last.)
+constexpr float kOpenLift = kTopP + 7.0f;
 constexpr int kScan = 512;             // sequences that a CTA sums
 constexpr int kEnter = 16;              // half pages that a further sequence's entry counts for
 
@@ -357,15 +363,16 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const __grid_const
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[j][i] = 0.0f;
-    // Of each row: the largest s + ev (s the base-2 score, ev the exponent of
-    // its value block's scale), the largest s, and the sum of 2^(s - ms).
+    // Of each row: the largest s + ev + lift (s the base-2 score, ev the exponent
+    // of its value block's scale), the largest s, and the sum of 2^(s - ms).
     float mt[2] = {-INFINITY, -INFINITY}, ms[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
     float ev_top = -INFINITY;
     bool vbad[2] = {false, false};
 
     // One half page's softmax on S, the products of q with the code values: s =
-    // S * c2 in the base-2 domain; P = 2^(s + ev - mt) back in sc.
-    auto softmax = [&](float (&sc)[4][4], int kbase, float c20, float c21, float ev, bool odd, bool none) {
+    // S * c2 in the base-2 domain; P = 2^(s + ev - mt + kTopP) back in sc, at most
+    // 2^(kTopP - lift).
+    auto softmax = [&](float (&sc)[4][4], int kbase, float c20, float c21, float ev, float lift, bool odd, bool none) {
       const bool partial = odd || kbase < all_lo || kbase + 32 > all_end;
       const float c2[2] = {c20, c21};
       float top[2] = {-INFINITY, -INFINITY};
@@ -391,14 +398,14 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const __grid_const
       bool grow = false;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float tn = fmaxf(mt[i], top[i] + ev), sn = fmaxf(ms[i], top[i]);
+        const float tn = fmaxf(mt[i], top[i] + (ev + lift)), sn = fmaxf(ms[i], top[i]);
         grow = grow || tn > mt[i];
         f[i] = mt[i] == -INFINITY ? 0.0f : ex2_ftz(mt[i] - tn);
         if (sn > ms[i]) l[i] *= ex2_ftz(ms[i] - sn);
         mt[i] = tn;
         ms[i] = sn;
         // A row that has seen no key keeps -inf: exp2(-inf - 0) = 0.
-        nt[i] = tn == -INFINITY ? 0.0f : -tn;
+        nt[i] = tn == -INFINITY ? 0.0f : kTopP - tn;
         ns[i] = sn == -INFINITY ? 0.0f : -sn;
       }
       if (__any_sync(0xffffffffu, grow)) {
@@ -474,7 +481,7 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const __grid_const
       const bool v_nan = isnan(vs);
       const float ev = v_nan ? 0.0f : pow2_log(vs);
       if (none && lane == 0) atomicOr(P.err, kErrRange);
-      softmax(sc, 32 * u, ks * q_factor[0], ks * q_factor[1], ev, none || isnan(ks), none);
+      softmax(sc, 32 * u, ks * q_factor[0], ks * q_factor[1], ev, 0.0f, none || isnan(ks), none);
       Run<D> vr[2][4];
 #pragma unroll
       for (int st2 = 0; st2 < 2; ++st2)
@@ -578,7 +585,7 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const __grid_const
           for (int y = 0; y < D / 64; ++y)
             vx[st][i][y] = __ldg(reinterpret_cast<const uint4*>(
                 vt + (16 * st + 2 * t + (i & 1) + 8 * (i >> 1)) * D + g * (D / 8) + 8 * y));
-      softmax(sc, 32 * u, P.scale_log2, P.scale_log2, 0.0f, false, false);
+      softmax(sc, 32 * u, P.scale_log2, P.scale_log2, 0.0f, kOpenLift, false, false);
       bool odd = false;                  // a value that is not finite
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
@@ -619,7 +626,7 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const __grid_const
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
       // O in units of 2^ms, like the sum.
-      const float unit = mt[i] == -INFINITY ? 1.0f : ex2_ftz(mt[i] - ms[i]);
+      const float unit = mt[i] == -INFINITY ? 1.0f : ex2_ftz(mt[i] - kTopP - ms[i]);
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll

@@ -125,6 +125,11 @@ __device__ __forceinline__ float pow2_inv(float s) {
   return __uint_as_float((254u << 23) - (__float_as_uint(s) & 0x7f800000u));
 }
 
+// P is held in fp16 times a power of two, 2^kTopP at the most: below 2^-14
+// fp16 has a fixed step of 2^-24, and the weights that a long row has many of may
+// be that small beside its largest.
+constexpr float kTopP = 15.0f;
+
 // What a query row sees, and where it is.  Row r of a (sequence, key head) is
 // query token r / group under query head h * group + r % group.
 struct CacheRow {
