@@ -454,11 +454,10 @@ salad_status salad_cache_append(const salad_cache_append_args* args, salad_strea
  * Closed blocks are read as their exact values (code * scale), so scales are
  * powers of two from 2^-100 up, or NaN with NaN codes, as the append writes
  * them.  Softmax statistics and sums are float32.  P is rounded for the
- * product with the values: to fp16 (by 2^-11 of itself; what is below 2^-14 of
- * a row's largest product of weight and block scale, by 2^-25 of that).  In
- * calls of few rows (64 of a key head at most) only what is below 2^-29 of
- * that product is rounded by more, by 2^-40 of it; and P is rounded to bf16
- * (2^-8) with the open block's values.
+ * product with the values: to fp16, by 2^-11 of itself, or, where it is below
+ * 2^-25 of a row's largest product of weight and block scale, by 2^-36 of that.
+ * In calls of few rows (64 of a key head at most) these are 2^-29 and 2^-40,
+ * and P is rounded to bf16 (2^-8) with the open block's values.
  * (Rows of a key head / 256) * (blocks / 2) stays below 2^31.  Workspace: salad_cache_attn_workspace_bytes(args); two calls
  * that may overlap on the GPU need two workspaces.
  */

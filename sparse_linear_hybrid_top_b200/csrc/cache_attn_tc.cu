@@ -15,9 +15,10 @@
 // two to a largest magnitude in [2^14, 2^15): its bf16 values stay exact down
 // to 2^-28 of that, and those below err by 2^-39 of it.  The open block's bf16
 // rows are scaled like a closed block's.  Key scales and the row's join the
-// softmax scale.  P, times the value block's scale, is at most 2^8 in fp16
-// (rounded by 2^-11); see the softmax for how its maximum and the row sum are
-// kept apart.
+// softmax scale.  P, times the value block's scale, is at most 2^15 in fp16:
+// rounded by 2^-11, or, 2^25 and more below the row's largest such product, by
+// 2^-36 of that (see the softmax for how its maximum and the row sum are kept
+// apart).
 //
 // Warp roles (512 threads, one CTA per SM):
 //   warps 0..3, 4..7   softmax and output of slots 0 and 1, a row per thread
@@ -59,6 +60,9 @@ namespace {
 constexpr int kRows = 256;            // query rows of an item
 constexpr int kTile = 128;            // keys of a tile
 constexpr int kThreads = 512;
+// What a row's products of weight and scale are counted against is raised to
+// 2^kBaseP where one passes 2^kTopP: they lie between the two, at their largest.
+constexpr float kBaseP = kTopP - 4.0f;
 // Registers of a thread: at launch, and the warpgroups' shares after it (two
 // of softmax warps, the converting one, the last).  Taking more than the
 // others give would wait forever.
@@ -855,10 +859,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
       if (mine) {
         const float c1 = P.scale_log2 * q_factor;
         // P = 2^(s + ev - mt), ev the exponent of the value block's scale and
-        // mt the row's largest s + ev (raised lazily, by more than 2^8 at a
-        // time): what a block adds to O is then rounded against the largest
-        // such product, however the scales differ.  The row sum l is kept
-        // against the largest score, ms.
+        // mt + kBaseP a recent largest s + ev of the row (raised by 2^4 and more at
+        // a time, which costs as little as 2^8; by 2^2 it took 4% more): what a
+        // block adds to O is then rounded against the largest such product,
+        // however the scales differ.  The row sum l is kept against the largest
+        // score, ms.
         float mt = -INFINITY, ms = -INFINITY, l = 0.0f;
         float ev_top = -INFINITY;                       // largest ev so far
         bool vbad = false;
@@ -910,9 +915,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
           }
           const float pm = fmaxf(s0 + ev0, s1 + ev1);
           float f = 1.0f;
-          if (pm > mt + 8.0f) {
-            f = mt == -INFINITY ? 1.0f : ex2_ftz(mt - pm);
-            mt = pm;
+          if (pm > mt + kTopP) {
+            f = mt == -INFINITY ? 1.0f : ex2_ftz(mt + kBaseP - pm);
+            mt = pm - kBaseP;
           }
           // The slot's previous PV was issued before this tile's QK, whose
           // commit has arrived: O may be rescaled.

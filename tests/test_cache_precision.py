@@ -8,7 +8,8 @@ max_i(p_i s_i), s_j the power-of-two scale of its values, is held in fp16 times
 a power of two: it is rounded by 2^-11 of itself, or by half of fp16's smallest
 step, 2^-25, where that is more.  With up to 64 rows of a key head the factor
 is 2^15, and the latter 2^-40 of the row's largest product; the open block's P
-is rounded to bf16, by 2^-8 of itself.
+is rounded to bf16, by 2^-8 of itself.  With more rows the factor is between
+2^11 and 2^15, and the open block is multiplied like a closed one.
 """
 import math
 
@@ -20,6 +21,7 @@ from tests.test_cache_attn import _held, _make, _q
 
 needs_gpu = pytest.mark.gpu
 FEW = dict(log_top=15, open_error=2.0 ** -8)
+MANY = dict(log_top=11, open_error=2.0 ** -11)
 
 
 def _bounded(cache, q, seq, log_top, open_error, o=None, frame=0, scale=None):
@@ -85,10 +87,10 @@ def _check_sink(d, n, rows, at, **kernel):
     q = _sink_queries(rows, d)
     cache, seq = _sink(256, d, n, at)
     o = salad.cache_attn(cache, q.expand(1, 256, rows, d), seq, scale=1.0)
-    assert bool((o == o[:, :1]).all())
     cache, seq = _sink(1, d, n, at)
-    o, want = _bounded(cache, q, seq, o=o[:, :1], scale=1.0, **kernel)
-    assert torch.all((o - want).abs() <= 0.02 * want.abs())
+    for h in (0, 100, 255):
+        got, want = _bounded(cache, q, seq, o=o[:, h:h + 1], scale=1.0, **kernel)
+        assert torch.all((got - want).abs() <= 0.02 * want.abs())
 
 
 @needs_gpu
@@ -121,3 +123,38 @@ def test_open_block_of_any_size_few_rows(rows):
         cache.v_tail[0, slot] *= 2.0 ** e
         cache.v_tail[0, slot, :, 37:] = 2.0 ** 127
         _bounded(cache, _q(1, 4, rows, 64, rows + 1), seq, **FEW)
+
+
+@needs_gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows", [70, 300])
+@pytest.mark.parametrize("at", [70, 8001 - 5])
+def test_many_small_weights_beside_one_large_many_rows(d, rows, at):
+    _check_sink(d, 8001, rows, at, **MANY)
+
+
+@needs_gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows,lens", [(70, [70, 128, 700]), (130, [190, 2111]), (300, [333, 1500])])
+def test_weights_many_rows(d, rows, lens):
+    cache, seq = _make(len(lens), 2, d, lens, seed=rows)
+    for frame in (0, 1):
+        _bounded(cache, _q(len(lens), 2, rows, d, rows), seq, frame=frame, **MANY)
+
+
+@needs_gpu
+@pytest.mark.parametrize("rows", [70, 300])
+def test_maxima_that_grow(rows):
+    """Scores that rise from block to block by less, and by more, than what a
+    row's maximum is raised at a time by."""
+    for step in (0.5, 2.0, 6.0, 20.0):
+        L = 64 * 12 + 17
+        g = torch.Generator().manual_seed(rows)
+        k = 0.25 * torch.randn(1, 1, L, 64, generator=g)
+        k[0, 0, :, 0] = (torch.arange(L) // 64) * step * math.log(2)
+        v = 1 + 0.25 * torch.randn(1, 1, L, 64, generator=g)
+        cache = salad.BlockCache.allocate(1, 1, 64, 13)
+        seq = salad.cache_append(cache, k.bfloat16().cuda(), v.bfloat16().cuda(), cache.new_seq())
+        q = torch.randn(1, 1, rows, 64, generator=g)
+        q[..., 0] = 1
+        _bounded(cache, q.bfloat16().cuda(), seq, scale=1.0, **MANY)
