@@ -446,6 +446,8 @@ salad_status salad_cache_append(const salad_cache_append_args* args, salad_strea
  *   window >= 0:   of the keys before the query's group (before the first
  *                  query, for frame = 0) only the last `window` are seen;
  *                  window < 0: all of them.
+ * Blocks that no row sees are not read: pages before the window of the first
+ * row may have been given back.
  * A row that sees no key (an empty sequence, or p < 0) is 0 with lse = -inf.
  * q, o: bf16 [B,Hq,N,d], strides as in salad_rope; Hq a multiple of the
  * cache's H, query head h reading key/value head h / (Hq / H).  lse (may be

@@ -541,10 +541,17 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
         int page;                                 // -2: not closed
         float ks, vs;
       };
-      // A table entry that is no page reads page 0; a key scale of 0 masks it.
+      // A table entry that is no page reads page 0; a key scale of 0 masks it.  So
+      // does the block of the item's first tile that lies before its rows' window:
+      // its page may have been given back.
       auto blocks_at = [&](const Seg& g, int blk) {
         Blocks k{-2, 1.0f, 1.0f};
-        if (blk + lane < g.s.len / kCacheBlock) {
+        const int lo =
+            cache_visible(g.s.len - g.s.count + g.tile * kRows / P.group, g.s.len, g.s.count, P.frame, P.window).lo;
+        if (blk + lane < lo / kCacheBlock) {
+          k.page = 0;
+          k.ks = 0.0f;
+        } else if (blk + lane < g.s.len / kCacheBlock) {
           k.page = cache_page(__ldg(P.c.page_table + static_cast<long long>(g.b) * P.c.blocks + blk + lane), P.c.pages);
           if (k.page < 0) {
             k.page = 0;
