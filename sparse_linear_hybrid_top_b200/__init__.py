@@ -558,6 +558,10 @@ class BlockCache:
     int32 [B, blocks].  The tensors are checked once, here, and used by every
     call; their contents are the program's to set and move (page_table above
     all).  ``allocate`` makes them.
+
+    Calls use the buffers' addresses, taken here once, so the attributes cannot
+    be assigned: a cache with a wider table or a larger pool is another
+    BlockCache over the new tensors (and those that stay).
     """
 
     BLOCK = 64
@@ -578,15 +582,24 @@ class BlockCache:
                          ("k_tail", k_tail, torch.bfloat16), ("v_tail", v_tail, torch.bfloat16),
                          ("page_table", page_table, torch.int32)):
             _dev_tensor(t, dt, n)
-        self.k_pages, self.v_pages, self.k_scale, self.v_scale = k_pages, v_pages, k_scale, v_scale
-        self.k_tail, self.v_tail, self.page_table = k_tail, v_tail, page_table
-        self.B, self.H, self.d, self.pages, self.blocks = B, H, d, pages, blocks
-        self.device = page_table.device
-        self.index = self.device.index
-        self.softmax_scale = 1.0 / math.sqrt(d)
-        # The fields of salad_cache, in order.
-        self.args = (_ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(k_tail),
-                     _ptr(v_tail), _ptr(page_table), B, H, d, pages, blocks)
+        buffers = dict(k_pages=k_pages, v_pages=v_pages, k_scale=k_scale, v_scale=v_scale, k_tail=k_tail,
+                       v_tail=v_tail, page_table=page_table)
+        # args: the fields of salad_cache, in order.
+        self.__dict__.update(buffers, B=B, H=H, d=d, pages=pages, blocks=blocks, device=page_table.device,
+                             index=page_table.device.index, softmax_scale=1.0 / math.sqrt(d),
+                             args=(*(_ptr(t) for t in buffers.values()), B, H, d, pages, blocks))
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"cannot assign {name}: calls use the addresses of the buffers that the BlockCache was "
+                             "made of; make another BlockCache over the new tensors")
+
+    def __delattr__(self, name):
+        self.__setattr__(name, None)
+
+    def __reduce__(self):
+        # A copy takes its own tensors' addresses.
+        return type(self), (self.k_pages, self.v_pages, self.k_scale, self.v_scale, self.k_tail, self.v_tail,
+                            self.page_table)
 
     @classmethod
     def allocate(cls, B: int, H: int, d: int, blocks: int, *, pages: Optional[int] = None,
