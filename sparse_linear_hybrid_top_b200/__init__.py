@@ -14,6 +14,7 @@ import struct
 from typing import Optional, Sequence
 
 import torch
+from torch.autograd import forward_ad
 
 __all__ = [
     "SaladError", "lib", "status_string", "version",
@@ -457,6 +458,26 @@ def _empty_on(stream, make):
         return make()
 
 
+def _no_grad(what: str, why: str, *tensors) -> None:
+    """Refuses a call whose gradient, or forward-mode tangent, would be lost
+    without a word.  tensors: inputs and outputs; None where there is none."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if isinstance(t, torch.Tensor) and t.requires_grad:
+                raise ValueError(f"{what} {why}")
+    # torch.no_grad() does not switch the forward mode off.
+    if forward_ad._current_level >= 0:
+        for t in tensors:
+            if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+                raise ValueError(f"{what} has no forward-mode derivative: call it on the dual tensors' primals")
+
+
+def _written(*tensors) -> None:
+    """Tells autograd that the call changed tensors of the caller: one that an
+    operator saved for its backward pass must not be used as if it had not."""
+    torch._C._increment_version(tensors)
+
+
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _PAIRINGS = {"adjacent": 0, "halves": 1}
 _NO_STRIDES = (0, 0, 0)
@@ -495,9 +516,8 @@ def _rope(what: str, q, k, positions, grid, offset, base, split, pairing, invers
     code = _DTYPES.get(dtype)
     if code is None:
         raise ValueError(f"q must be bfloat16, float16 or float32, got {dtype}")
-    if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
-        raise ValueError(f"{what} is not recorded by autograd: call it under torch.no_grad() and "
-                         "turn the gradients with rope_backward")
+    _no_grad(what, "is not recorded by autograd: call it under torch.no_grad() and turn the gradients with "
+             "rope_backward", q, k, q_out, k_out)
     shape = q.shape
     B, Hq, N, d = shape
     q_st = _rows(q, shape, dtype, dev, "q")
@@ -520,7 +540,11 @@ def _rope(what: str, q, k, positions, grid, offset, base, split, pairing, invers
     a = _pack(_PACK_ROPE, what, q.data_ptr(), q_out.data_ptr(), kp, kop, *q_st, *qo_st, *k_st, *ko_st, code, B,
               Hq, Hk, N, d, at, batched, Hh, Wh, offset, *split, base, pair, inverse)
     _check(lib.salad_rope(a, _stream_on(stream, dev)), what)
-    return q_out if k is None else (q_out, k_out)
+    if k is None:
+        _written(q_out)
+        return q_out
+    _written(q_out, k_out)
+    return q_out, k_out
 
 
 def rope(q: torch.Tensor, k: Optional[torch.Tensor] = None, *, positions=None, grid=None,
@@ -584,10 +608,11 @@ class BlockCache:
             _dev_tensor(t, dt, n)
         buffers = dict(k_pages=k_pages, v_pages=v_pages, k_scale=k_scale, v_scale=v_scale, k_tail=k_tail,
                        v_tail=v_tail, page_table=page_table)
-        # args: the fields of salad_cache, in order.
+        # args: the fields of salad_cache, in order; held: what an append writes.
         self.__dict__.update(buffers, B=B, H=H, d=d, pages=pages, blocks=blocks, device=page_table.device,
                              index=page_table.device.index, softmax_scale=1.0 / math.sqrt(d),
-                             args=(*(_ptr(t) for t in buffers.values()), B, H, d, pages, blocks))
+                             args=(*(_ptr(t) for t in buffers.values()), B, H, d, pages, blocks),
+                             held=(k_pages, v_pages, k_scale, v_scale, k_tail, v_tail))
 
     def __setattr__(self, name, value):
         raise AttributeError(f"cannot assign {name}: calls use the addresses of the buffers that the BlockCache was "
@@ -622,6 +647,9 @@ class BlockCache:
         return torch.zeros(self.B, 2, dtype=torch.int32, device=self.device)
 
 
+_NO_BACKWARD = "has no backward pass: call it under torch.no_grad()"
+
+
 def _cache_call(cache, seq, counts):
     """(device index, address of seq, address of counts) of a call on a cache."""
     if not isinstance(cache, BlockCache):
@@ -631,12 +659,6 @@ def _cache_call(cache, seq, counts):
         raise ValueError(f"cache is on {cache.device}, but the current device is cuda:{dev}")
     return (dev, _flat(seq, (cache.B, 2), torch.int32, dev, "seq"),
             0 if counts is None else _flat(counts, (cache.B,), torch.int32, dev, "counts"))
-
-
-def _no_grad(what: str, *tensors) -> None:
-    """Refuses a call whose gradient would be lost without a word."""
-    if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
-        raise ValueError(f"{what} has no backward pass: call it under torch.no_grad()")
 
 
 def cache_append(cache: BlockCache, k: torch.Tensor, v: torch.Tensor, seq: torch.Tensor, *,
@@ -659,7 +681,7 @@ def cache_append(cache: BlockCache, k: torch.Tensor, v: torch.Tensor, seq: torch
     N = k.shape[2]
     shape = (cache.B, cache.H, N, cache.d)
     k_st, v_st = _rows(k, shape, torch.bfloat16, dev, "k"), _rows(v, shape, torch.bfloat16, dev, "v")
-    _no_grad("salad_cache_append", k, v)
+    _no_grad("salad_cache_append", _NO_BACKWARD, k, v, *cache.held)
     rotate = positions is not None or grid is not None
     if rotate:
         split, pair, at, batched, Hh, Wh = _rotation(cache.d, split, pairing, positions, grid, cache.B, N, dev)
@@ -671,6 +693,7 @@ def cache_append(cache: BlockCache, k: torch.Tensor, v: torch.Tensor, seq: torch
     a = _pack(_PACK_APPEND, "salad_cache_append", *cache.args, seq_ptr, out_ptr, k.data_ptr(), v.data_ptr(), *k_st,
               *v_st, N, counts_ptr, rotate, at, batched, Hh, Wh, *split, base, pair)
     _check(lib.salad_cache_append(a, _stream_on(stream, dev)), "salad_cache_append")
+    _written(seq_out, *cache.held)
     return seq_out
 
 
@@ -693,7 +716,7 @@ def cache_attn(cache: BlockCache, q: torch.Tensor, seq: torch.Tensor, *, counts=
     Hq, N = q.shape[1:3]
     shape = (cache.B, Hq, N, cache.d)
     q_st = _rows(q, shape, torch.bfloat16, dev, "q")
-    _no_grad("salad_cache_attn", q)
+    _no_grad("salad_cache_attn", _NO_BACKWARD, q, o, lse, *cache.held)
     if o is None:
         o = _empty_on(stream, lambda: torch.empty_like(q))
     o_st = _rows(o, shape, torch.bfloat16, dev, "o")
@@ -706,6 +729,10 @@ def cache_attn(cache: BlockCache, q: torch.Tensor, seq: torch.Tensor, *, counts=
         ws = _empty_on(stream, lambda: _workspace(need, q.device, workspace))
         a = _PACK_ATTN.pack(*head, ws.data_ptr(), ws.numel() * ws.element_size())
     _check(lib.salad_cache_attn(a, _stream_on(stream, dev)), "salad_cache_attn")
+    if lse is None:
+        _written(o)
+    else:
+        _written(o, lse)
     return o
 
 
