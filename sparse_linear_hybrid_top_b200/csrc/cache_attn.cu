@@ -625,18 +625,19 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const __grid_const
     for (int i = 0; i < 2; ++i) {
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-      // O in units of 2^ms, like the sum.
+      // The rows' means: sums of large values need not be a float.
+      const float inv = weight_inv(l[i]);
       const float unit = mt[i] == -INFINITY ? 1.0f : ex2_ftz(mt[i] - kTopP - ms[i]);
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) o[j][2 * i + e] = vbad[i] ? __int_as_float(0x7fffffff) : o[j][2 * i + e] * unit;
+        for (int e = 0; e < 2; ++e) o[j][2 * i + e] = vbad[i] ? __int_as_float(0x7fffffff) : o[j][2 * i + e] * inv * unit;
     }
 
     // ---- merge the CTA's key groups, then write the rows (or their part, in
     // the place of (CTA + sequence): one of the two grows from part to part)
     auto put = [&](int r, const float* acc, float mm, float ll, int c0, int nc) {
-      // acc: nc channels from c0 of row r, unnormalised.
+      // acc: nc channels from c0 of row r.
       const CacheRow x = cache_row(P, r, h, s.len, count);
       if (!x.valid) return;
       if (!whole) {
@@ -648,13 +649,12 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const __grid_const
           *reinterpret_cast<float4*>(to + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
         return;
       }
-      const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
       char* to = P.o + b * P.ob + x.head * P.oh + x.n * P.on + 2 * c0;
 #pragma unroll
       for (int c = 0; c < nc; c += 8)
         *reinterpret_cast<uint4*>(to + 2 * c) =
-            make_uint4(pack_bf16x2(acc[c] * inv, acc[c + 1] * inv), pack_bf16x2(acc[c + 2] * inv, acc[c + 3] * inv),
-                       pack_bf16x2(acc[c + 4] * inv, acc[c + 5] * inv), pack_bf16x2(acc[c + 6] * inv, acc[c + 7] * inv));
+            make_uint4(pack_bf16x2(acc[c], acc[c + 1]), pack_bf16x2(acc[c + 2], acc[c + 3]),
+                       pack_bf16x2(acc[c + 4], acc[c + 5]), pack_bf16x2(acc[c + 6], acc[c + 7]));
       if (c0 == 0 && P.lse != nullptr)
         P.lse[(static_cast<long long>(b) * P.Hq + x.head) * P.N + x.n] = (mm + log2f(ll)) * 0.6931471805599453f;
     };
@@ -686,20 +686,16 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const __grid_const
       for (int e = threadIdx.x; e < RW * 16 * (D / 8); e += kThreads) {
         const int r = e / (D / 8), c0 = e % (D / 8) * 8;
         const int w = r / 16, rr = r % 16;
-        float mm = -INFINITY, ll = 0.0f, acc[8] = {};
+        float mm = -INFINITY, ll = 0.0f, f[KW], acc[8] = {};
 #pragma unroll
         for (int k = 0; k < KW; ++k) mm = fmaxf(mm, mls[w][k][rr].x);
 #pragma unroll
-        for (int k = 0; k < KW; ++k) {
-          const float2 p = mls[w][k][rr];
-          // A part that saw no key (its sum is 0) counts for nothing; one whose
-          // sum is NaN does.
-          if (p.y == 0.0f) continue;
-          const float f = p.x == -INFINITY ? 1.0f : ex2_ftz(p.x - mm);
-          ll = fmaf(p.y, f, ll);
+        for (int k = 0; k < KW; ++k) ll += f[k] = part_weight(mls[w][k][rr], mm);
+        const float inv = weight_inv(ll);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) acc[c] = fmaf(os[w][k][rr][c0 + c], f, acc[c]);
-        }
+        for (int k = 0; k < KW; ++k)
+#pragma unroll
+          for (int c = 0; c < 8; ++c) acc[c] = fmaf(os[w][k][rr][c0 + c], f[k] * inv, acc[c]);
         put(r, acc, mm, ll, c0, 8);
       }
     }
@@ -742,8 +738,6 @@ __global__ void __launch_bounds__(kThreads) cache_merge_kernel(const __grid_cons
       for (int c = 0; c < C; ++c) v[i][c] = k + i < nw ? from[(k + i) * step * D + c] : 0.0f;
   };
   load(0);
-  // A part's weight against the warp's largest maximum, 0 where it saw no key
-  // (its O is 0 too).
   float2 p[kMergeLane];
   float mm = -INFINITY;
 #pragma unroll
@@ -753,47 +747,47 @@ __global__ void __launch_bounds__(kThreads) cache_merge_kernel(const __grid_cons
   }
 #pragma unroll
   for (int i = 16; i > 0; i /= 2) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, i));
-  auto weight = [](float2 x, float top) { return x.y == 0.0f ? 0.0f : (x.x == -INFINITY ? 1.0f : ex2_ftz(x.x - top)); };
-  float ll = 0.0f, acc[C] = {};
+  // The parts' weights, and the warp's mean.
+  float w[kMergeLane], ll = 0.0f, acc[C] = {};
+#pragma unroll
+  for (int i = 0; i < kMergeLane; ++i) ll += w[i] = part_weight(p[i], mm);
+#pragma unroll
+  for (int i = 16; i > 0; i /= 2) ll += __shfl_xor_sync(0xffffffffu, ll, i);
+  const float inv = weight_inv(ll);
 #pragma unroll
   for (int i = 0; i < kMergeLane; ++i) {
-    const float w = weight(p[i], mm);
-    ll = fmaf(p[i].y, w, ll);
     for (int k = 32 * i; k < min(nw, 32 * i + 32); k += FLY) {
       if (k > 0) load(k);
 #pragma unroll
       for (int j = 0; j < FLY; ++j) {
-        const float f = __shfl_sync(0xffffffffu, w, (k + j) % 32);
+        const float f = __shfl_sync(0xffffffffu, w[i] * inv, (k + j) % 32);
 #pragma unroll
         for (int c = 0; c < C; ++c) acc[c] = fmaf(v[j][c], f, acc[c]);
       }
     }
   }
 #pragma unroll
-  for (int i = 16; i > 0; i /= 2) ll += __shfl_xor_sync(0xffffffffu, ll, i);
-#pragma unroll
   for (int c = 0; c < C; ++c) os[warp][lane * C + c] = acc[c];
   if (lane == 0) mls[warp] = make_float2(mm, ll);
   __syncthreads();
   if (warp > 0) return;
   mm = fmaxf(fmaxf(mls[0].x, mls[1].x), fmaxf(mls[2].x, mls[3].x));
-  ll = 0.0f;
+  float sum = 0.0f, f[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) sum += f[k] = part_weight(mls[k], mm);
 #pragma unroll
   for (int c = 0; c < C; ++c) acc[c] = 0.0f;
+  const float all = weight_inv(sum);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float f = weight(mls[k], mm);
-    ll = fmaf(mls[k].y, f, ll);
+  for (int k = 0; k < 4; ++k)
 #pragma unroll
-    for (int c = 0; c < C; ++c) acc[c] = fmaf(os[k][lane * C + c], f, acc[c]);
-  }
-  const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+    for (int c = 0; c < C; ++c) acc[c] = fmaf(os[k][lane * C + c], f[k] * all, acc[c]);
   char* to = P.o + b * P.ob + head * P.oh + i_q * P.on + 2 * lane * C;
 #pragma unroll
   for (int c = 0; c < C; c += 2)
-    *reinterpret_cast<uint32_t*>(to + 2 * c) = pack_bf16x2(acc[c] * inv, acc[c + 1] * inv);
+    *reinterpret_cast<uint32_t*>(to + 2 * c) = pack_bf16x2(acc[c], acc[c + 1]);
   if (lane == 0 && P.lse != nullptr)
-    P.lse[(static_cast<long long>(b) * P.Hq + head) * P.N + i_q] = (mm + log2f(ll)) * 0.6931471805599453f;
+    P.lse[(static_cast<long long>(b) * P.Hq + head) * P.N + i_q] = (mm + log2f(sum)) * 0.6931471805599453f;
 }
 
 // Row warps and CTAs per head of a call.

@@ -22,7 +22,7 @@ struct CacheAttnParams {
   int frame, window;
   float scale_log2;                   // softmax scale * log2(e)
   int tiles;                          // row tiles of one (sequence, key head)
-  float* part_o;                      // unnormalised parts of rows, for the merging launch
+  float* part_o;                      // means of parts of rows, for the merging launch
   float2* part_ml;                    // their maxima and sums
   int2* plan;                         // [B], first CTA of a sequence's parts, and how many
   unsigned* err;
@@ -117,6 +117,13 @@ __device__ __forceinline__ float ex2_ftz(float x) {
   return y;
 }
 
+// 1 / x of a sum of weights, 0 for a row that has none.
+__device__ __forceinline__ float weight_inv(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return x == 0.0f ? 0.0f : y;
+}
+
 // log2 and reciprocal of a power of two (exponent bits only).
 __device__ __forceinline__ float pow2_log(float s) {
   return static_cast<float>(static_cast<int>((__float_as_uint(s) >> 23) & 255u) - 127);
@@ -129,6 +136,14 @@ __device__ __forceinline__ float pow2_inv(float s) {
 // fp16 has a fixed step of 2^-24, and the weights that a long row has many of may
 // be that small beside its largest.
 constexpr float kTopP = 15.0f;
+
+// The weight of a part of a row: its sum (of 2^(s - x)) against a maximum of
+// `top`.  A part that saw no key (its sum is 0) counts for nothing; one whose sum
+// is NaN does.
+__device__ __forceinline__ float part_weight(float2 part, float top) {
+  if (part.y == 0.0f) return 0.0f;
+  return part.x == -INFINITY ? part.y : part.y * ex2_ftz(part.x - top);
+}
 
 // What a query row sees, and where it is.  Row r of a (sequence, key head) is
 // query token r / group under query head h * group + r % group.

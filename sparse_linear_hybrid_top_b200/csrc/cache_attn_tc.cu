@@ -1044,7 +1044,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
         const bool whole = g.t0 == 0 && g.t1 == g.all.n;
         const bool odd = odd_seg[part_no % 8] == part_no + 1;
         const float unit = mt == -INFINITY ? 1.0f : ex2_ftz(mt - ms);
-        const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+        // Means, of parts too: sums of large values need not be a float.
+        const float inv = weight_inv(l);
         char* orow = P.o + g.b * P.ob + row.head * P.oh + row.n * P.on;
         const long long part = 2ll * blockIdx.x + (g.first ? 0 : 1);
 #pragma unroll 1
@@ -1053,7 +1054,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
           tmem_ld32(obuf + c0, o32);
           float v[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = vbad ? __int_as_float(0x7fffffff) : __uint_as_float(o32[e]) * unit;
+          for (int e = 0; e < 32; ++e) v[e] = vbad ? __int_as_float(0x7fffffff) : __uint_as_float(o32[e]) * inv * unit;
           if (odd && row.valid) {
             const int first = g.s.len / kCacheBlock * kCacheBlock;
             const __nv_bfloat16* tail = static_cast<const __nv_bfloat16*>(P.c.v_tail) +
@@ -1069,8 +1070,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
 #pragma unroll
             for (int e = 0; e < 32; e += 8)
               *reinterpret_cast<uint4*>(orow + 2 * (c0 + e)) =
-                  make_uint4(pack_bf16x2(v[e] * inv, v[e + 1] * inv), pack_bf16x2(v[e + 2] * inv, v[e + 3] * inv),
-                             pack_bf16x2(v[e + 4] * inv, v[e + 5] * inv), pack_bf16x2(v[e + 6] * inv, v[e + 7] * inv));
+                  make_uint4(pack_bf16x2(v[e], v[e + 1]), pack_bf16x2(v[e + 2], v[e + 3]),
+                             pack_bf16x2(v[e + 4], v[e + 5]), pack_bf16x2(v[e + 6], v[e + 7]));
           } else if (row.valid) {
             // [part][channel][row]: a warp's rows side by side.
             float* to = P.part_o + (part * D + c0) * kRows + slot * 128 + r;
@@ -1143,17 +1144,16 @@ __global__ void __launch_bounds__(256) cache_tc_merge_kernel(const __grid_consta
   // The item is the first part of every CTA but, perhaps, its first one's.
   const int first_part = total * c0 / ctas >= in.start ? 0 : 1;
   auto part_of = [&](int c) { return 2ll * c + (c == c0 ? first_part : 0); };
-  // A part that saw no key has a sum of 0 (and an O of 0).
-  auto weight = [](float2 p, float top) { return p.y == 0.0f ? 0.0f : (p.x == -INFINITY ? 1.0f : ex2_ftz(p.x - top)); };
   float m = -INFINITY;
 #pragma unroll 4
   for (int c = c_first; c <= c1; c += split) m = fmaxf(m, P.part_ml[part_of(c) * kRows + r0 + lane].x);
   float l = 0.0f, acc[C] = {};
+#pragma unroll 4
+  for (int c = c_first; c <= c1; c += split) l += part_weight(P.part_ml[part_of(c) * kRows + r0 + lane], m);
+  const float inv = weight_inv(l);
 #pragma unroll 2
   for (int c = c_first; c <= c1; c += split) {
-    const float2 p = P.part_ml[part_of(c) * kRows + r0 + lane];
-    const float f = weight(p, m);
-    l = fmaf(p.y, f, l);
+    const float f = part_weight(P.part_ml[part_of(c) * kRows + r0 + lane], m) * inv;
     const float* from = P.part_o + (part_of(c) * D + ch) * kRows + r0 + lane;
 #pragma unroll
     for (int e = 0; e < C; ++e) acc[e] = fmaf(from[e * kRows], f, acc[e]);
@@ -1162,13 +1162,12 @@ __global__ void __launch_bounds__(256) cache_tc_merge_kernel(const __grid_consta
     // The row's sums are all here.
     const CacheRow row = cache_row(P, in.tile * kRows + r0 + lane, in.h, s.len, s.count);
     if (!row.valid) return;
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     char* to = P.o + in.b * P.ob + row.head * P.oh + row.n * P.on + 2 * ch;
 #pragma unroll
     for (int e = 0; e < C; e += 8)
       *reinterpret_cast<uint4*>(to + 2 * e) =
-          make_uint4(pack_bf16x2(acc[e] * inv, acc[e + 1] * inv), pack_bf16x2(acc[e + 2] * inv, acc[e + 3] * inv),
-                     pack_bf16x2(acc[e + 4] * inv, acc[e + 5] * inv), pack_bf16x2(acc[e + 6] * inv, acc[e + 7] * inv));
+          make_uint4(pack_bf16x2(acc[e], acc[e + 1]), pack_bf16x2(acc[e + 2], acc[e + 3]),
+                     pack_bf16x2(acc[e + 4], acc[e + 5]), pack_bf16x2(acc[e + 6], acc[e + 7]));
     if (ch == 0 && P.lse != nullptr)
       P.lse[(static_cast<long long>(in.b) * P.Hq + row.head) * P.N + row.n] = (m + log2f(l)) * 0.6931471805599453f;
     return;
@@ -1185,15 +1184,15 @@ __global__ void __launch_bounds__(256) cache_tc_merge_kernel(const __grid_consta
     if (!row.valid) continue;
     float top = -INFINITY, sum = 0.0f, a0 = 0.0f, a1 = 0.0f;
     for (int k = g; k < 8; k += groups) top = fmaxf(top, mls[k][i].x);
+    for (int k = g; k < 8; k += groups) sum += part_weight(mls[k][i], top);
+    const float all = weight_inv(sum);
     for (int k = g; k < 8; k += groups) {
-      const float f = weight(mls[k][i], top);
-      sum = fmaf(mls[k][i].y, f, sum);
+      const float f = part_weight(mls[k][i], top) * all;
       a0 = fmaf(os[k][e][i], f, a0);
       a1 = fmaf(os[k][e + 1][i], f, a1);
     }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     *reinterpret_cast<uint32_t*>(P.o + in.b * P.ob + row.head * P.oh + row.n * P.on + 2 * (ch0 + g * C + e)) =
-        pack_bf16x2(a0 * inv, a1 * inv);
+        pack_bf16x2(a0, a1);
     if (ch0 == 0 && pair == 0 && P.lse != nullptr)
       P.lse[(static_cast<long long>(in.b) * P.Hq + row.head) * P.N + row.n] = (top + log2f(sum)) * 0.6931471805599453f;
   }

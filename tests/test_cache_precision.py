@@ -158,3 +158,25 @@ def test_maxima_that_grow(rows):
         q = torch.randn(1, 1, rows, 64, generator=g)
         q[..., 0] = 1
         _bounded(cache, q.bfloat16().cuda(), seq, scale=1.0, **MANY)
+
+
+@needs_gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows,H", [(1, 1), (1, 40), (20, 2), (60, 2), (70, 1), (300, 2)])
+def test_values_near_the_largest_and_the_smallest(d, rows, H):
+    """Means of values up to 2^127, whose sums are not floats, and of values
+    around 2^-95: in the open block alone, in one CTA and in many."""
+    kernel = MANY if rows > 64 else FEW
+    g = torch.Generator().manual_seed(d + rows)
+    for L in (rows + 20, rows + 300, 3001):
+        k = torch.randn(1, H, L, d, generator=g)
+        v = 1 - torch.randint(0, 3, (1, H, L, d), generator=g) / 4
+        q = _q(1, H, rows, d, L)
+        for size in (2.0 ** 127, 2.0 ** -95):
+            cache = salad.BlockCache.allocate(1, H, d, L // 64 + 1)
+            seq = salad.cache_append(cache, k.bfloat16().cuda(), (v * size).bfloat16().cuda(), cache.new_seq())
+            if H == 40:
+                o = salad.cache_attn(cache, q, seq)
+                assert torch.all((o.double() <= size) & (o.double() >= size / 2))
+            else:
+                _bounded(cache, q, seq, **kernel)
