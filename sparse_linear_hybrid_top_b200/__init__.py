@@ -496,6 +496,8 @@ def _rotation(d: int, split, pairing: str, positions, grid, B: int, N: int, dev:
     if (positions is None) == (grid is None):
         raise ValueError("give the tokens' positions or their grid")
     if positions is None:
+        if len(grid) != 2:
+            raise ValueError("grid must be (Hh, Wh), the height and the width of a latent frame")
         return split, pair, 0, 0, grid[0], grid[1]
     batched = int(isinstance(positions, torch.Tensor) and positions.dim() == 3)
     return (split, pair, _flat(positions, (B, N, 3) if batched else (N, 3), torch.int32, dev, "positions"), batched,
