@@ -24,8 +24,10 @@ FEW = dict(log_top=15, open_error=2.0 ** -8)
 MANY = dict(log_top=11, open_error=2.0 ** -11)
 
 
-def _bounded(cache, q, seq, log_top, open_error, o=None, frame=0, scale=None):
-    """Checks o (default: the call's output) against the bound, row by row."""
+def _bounded(cache, q, seq, log_top, open_error, o=None, frame=0, scale=None, held=None):
+    """Checks o (default: the call's output) against the bound, row by row.
+    held: keys, values and the values' scales of every sequence, where they are
+    known otherwise than from the cache."""
     B, Hq, N, d = q.shape
     if o is None:
         o = salad.cache_attn(cache, q, seq, frame=frame, scale=scale)
@@ -35,7 +37,7 @@ def _bounded(cache, q, seq, log_top, open_error, o=None, frame=0, scale=None):
     want = torch.zeros_like(o)
     worst = 0.0
     for b in range(B):
-        k, v, vs = _held(cache, seq, b)
+        k, v, vs = _held(cache, seq, b) if held is None else held[b]
         L = k.shape[1]
         closed = torch.arange(L) < L // 64 * 64
         for h in range(Hq):
@@ -180,3 +182,59 @@ def test_values_near_the_largest_and_the_smallest(d, rows, H):
                 assert torch.all((o.double() <= size) & (o.double() >= size / 2))
             else:
                 _bounded(cache, q, seq, **kernel)
+
+
+def _as_held(x):
+    """What a cache holds of x (bf16 [H, n, d]) and its scales [H, n], from the
+    rule alone: full blocks of 64 tokens in e4m3, times the smallest 2^e for which
+    none of the head's values passes 448 * 2^e; the rest as it is."""
+    x = x.cpu().double()
+    H, n, d = x.shape
+    out, scales = x.clone(), torch.ones(H, n, dtype=torch.float64)
+    for j in range(0, n, 64):
+        block = x[:, j:j + 64]
+        e = torch.log2(block.abs().amax((1, 2)) / 448).ceil()
+        e += (block.abs().amax((1, 2)) > 448 * torch.exp2(e)).double()
+        scales[:, j:j + 64] = torch.exp2(e)[:, None]
+        if block.shape[1] == 64:
+            s = torch.exp2(e)[:, None, None]
+            out[:, j:j + 64] = (block / s).float().to(torch.float8_e4m3fn).double() * s
+    return out, scales
+
+
+@needs_gpu
+@pytest.mark.parametrize("Hh,Wh,kernel", [(4, 5, FEW), (8, 12, MANY)])
+def test_chunk_by_chunk_generation_against_dense_attention(Hh, Wh, kernel):
+    """Three frames at a time, appended twice and attended frame by frame, against
+    dense attention over all keys and values so far, turned by salad_rope and
+    rounded by the cache's rule, which never saw the cache.  The bound tells the
+    blocks' places: it does not hold with the values of two exchanged, nor with
+    two of different frames exchanged whole."""
+    H, d, F, plane = 3, 128, 12, Hh * Wh
+    cache = salad.BlockCache.allocate(1, H, d, (F * plane + 63) // 64)
+    cache.page_table.copy_(cache.page_table.flip(1))
+    seq = cache.new_seq()
+    g = torch.Generator().manual_seed(plane)
+    q, k, v = (torch.randn(1, H, F * plane, d, generator=g).to(torch.bfloat16).cuda() for _ in range(3))
+    turned = salad.rope(k, grid=(Hh, Wh))
+    for f in range(0, F, 3):
+        part = slice(f * plane, (f + 3) * plane)
+        qr = salad.rope(q[:, :, part], grid=(Hh, Wh), offset=f * plane)
+        for _ in range(2):
+            after = salad.cache_append(cache, k[:, :, part], v[:, :, part], seq, grid=(Hh, Wh))
+        seq = after
+        kh, _ = _as_held(turned[0, :, :part.stop])
+        vh, vs = _as_held(v[0, :, :part.stop])
+        o, _ = _bounded(cache, qr, seq, frame=plane, held=[(kh, vh, vs)], **kernel)
+
+    def exchanged(x, i, j):
+        x = x.clone()
+        x[:, 64 * i:64 * i + 64], x[:, 64 * j:64 * j + 64] = x[:, 64 * j:64 * j + 64].clone(), x[:, 64 * i:64 * i + 64].clone()
+        return x
+
+    wrong = [(kh, exchanged(vh, 0, 1), exchanged(vs, 0, 1))]
+    if plane > 64:
+        wrong.append(tuple(exchanged(x, F * plane // 64 - 4, F * plane // 64 - 1) for x in (kh, vh, vs)))
+    for held in wrong:
+        with pytest.raises(AssertionError):
+            _bounded(cache, qr, seq, o=o, frame=plane, held=[held], **kernel)
