@@ -458,10 +458,14 @@ salad_status salad_cache_append(const salad_cache_append_args* args, salad_strea
  * them.  Softmax statistics and sums are float32.  P is rounded for the
  * product with the values: to fp16, by 2^-11 of itself, or, where it is below
  * 2^-25 of a row's largest product of weight and block scale, by 2^-36 of that.
- * In calls of few rows (64 of a key head at most) these are 2^-29 and 2^-40,
- * and P is rounded to bf16 (2^-8) with the open block's values.
- * (Rows of a key head / 256) * (blocks / 2) stays below 2^31.  Workspace: salad_cache_attn_workspace_bytes(args); two calls
- * that may overlap on the GPU need two workspaces.
+ * In calls of few rows (up to 32 of a key head, and up to 64 where
+ * B * H * blocks is small) these are 2^-29 and 2^-40, and P is rounded to bf16
+ * (2^-8) with the open block's values: with 33 to 64 rows the width of the
+ * table decides, and with it the last bits.  In calls of few rows on more than
+ * 512 sequences the keys of a sequence and head are not split over the GPU.
+ * (Rows of a key head / 256) * (blocks / 2) stays below 2^31.  Workspace:
+ * salad_cache_attn_workspace_bytes(args); two calls that may overlap on the
+ * GPU need two workspaces.
  */
 typedef struct salad_cache_attn_args {
     salad_cache cache;

@@ -41,11 +41,11 @@
 // whole is written at once, the parts of the others are merged by a second
 // launch.
 //
-// Measured (d = 128): one token, 12 heads, 31200 keys 29.8 us, 124800 keys 73.6
+// Measured (d = 128): one token, 12 heads, 31200 keys 29.7 us, 124800 keys 73.6
 // us (5.2 TB/s; 14 us are launches, the chain lengths - table - pages - rows, and
-// the merge); 16 tokens on 31200 keys 30.7 us, 32 49 us, where the second tile's
-// products and exponentials take longer than the memory; 16 unequal sequences of
-// 40 heads on 8 65.5 us (4.4 TB/s).
+// the merge); 16 tokens on 31200 keys 30.7 us, 32 47 us: there each of the two row
+// warps converts the same codes, and two key groups have half of four's chains;
+// 16 unequal sequences of 40 heads on 8 66.0 us (4.3 TB/s).
 #include "cache_attn.cuh"
 
 namespace salad {
@@ -867,6 +867,8 @@ cudaError_t launch_d(const Ctx& c, const CacheAttnParams& P, const Shape& s) {
 // with more than 32 where the tables have room for much work.  At 33 to 64 rows
 // (64 here, 65 there; 12 heads) 1000 keys take 25 us and 27, 7800 36 and 38,
 // 31200 82 and 75; 60 rows, 8 heads and 16 sequences of 8640 keys 234 and 154.
+// Both are far from the 14.6 us that reading 31200 keys takes: neither shares a
+// converted tile among as many warps as the rows leave room for.
 // Lengths are not known here; a table much wider than its sequences costs the
 // difference of the short ones.  At 17 to 32 rows this one is ahead at any
 // length (31200 keys: 49 and 75).

@@ -33,16 +33,18 @@
 // While the tensor pipe runs one slot's PV(t) and QK(t+1), the other slot's
 // softmax runs.  P overwrites S in TMEM.
 //
-// Measured (d = 128): 4680 query tokens (three frames of 1560) on 23400 keys, 12
-// heads, 558 us; 3600 on 104400, 8 heads, 1.72 ms: 880 and 860 TFLOP/s, 0.53 and
-// 0.52 of the burst rate of a large matrix product.  A pair of tiles takes 1.75
-// times its products' cycles.  No unit bounds it alone (timed with parts left
+// Measured (d = 128): 4680 query tokens (three frames of 1560) on 18720 keys,
+// their own among them and masked by frame, 12 heads, 562 to 568 us; 3600 on 100800,
+// 8 heads, 1.74 ms: 870 and 855 TFLOP/s, 0.52 of the burst rate of a large matrix
+// product.  A pair of tiles takes 1.75 times its products' cycles.  No unit bounds it alone (timed with parts left
 // out: without the exponentials 0.85 of the time, without the conversion 0.9,
 // with an eighth of the products 0.83): the way of a slot, S - maximum -
 // exponentials - P - PV - QK, is as long as two slots' products, and TMEM has no
 // room for a third.  For 3600 on 50400 keys the turns at the exponentials (see
 // the softmax) brought 970 us to 857; 16 softmax warps, two to a row, took 871
-// to 891.
+// to 891.  An item of 128 rows and fewer leaves one slot idle, and the other has
+// nothing beside its steps: 65 rows on 31200 keys of 12 heads take 77 us, where
+// reading the cache takes 14.6 (the tensor pipe is active for 16% of it).
 //
 // Balance: lengths are known on the device only, and tiles per item differ by
 // frame.  A first launch sums the items' tiles; every CTA then takes an equal
