@@ -585,12 +585,14 @@ class BlockCache:
     call; their contents are the program's to set and move (page_table above
     all).  ``allocate`` makes them.
 
-    Calls use the buffers' addresses, taken here once, so the attributes cannot
-    be assigned: a cache with a wider table or a larger pool is another
-    BlockCache over the new tensors (and those that stay).
+    Calls use the buffers' addresses, taken here once, so these attributes and
+    the sizes cannot be assigned: a cache with a wider table or a larger pool is
+    another BlockCache over the new tensors (and those that stay).
     """
 
     BLOCK = 64
+    _FIXED = frozenset(("k_pages", "v_pages", "k_scale", "v_scale", "k_tail", "v_tail", "page_table", "B", "H", "d",
+                        "pages", "blocks", "device", "index", "args", "held"))
 
     def __init__(self, k_pages, v_pages, k_scale, v_scale, k_tail, v_tail, page_table):
         _dims(k_pages, 4, "k_pages", "[pages, H, 64, d]")
@@ -616,17 +618,23 @@ class BlockCache:
                              args=(*(_ptr(t) for t in buffers.values()), B, H, d, pages, blocks),
                              held=(k_pages, v_pages, k_scale, v_scale, k_tail, v_tail))
 
+    def _changeable(self, name):
+        if name in self._FIXED:
+            raise AttributeError(f"cannot assign {name}: calls use the addresses of the buffers that the BlockCache "
+                                 "was made of; make another BlockCache over the new tensors")
+
     def __setattr__(self, name, value):
-        raise AttributeError(f"cannot assign {name}: calls use the addresses of the buffers that the BlockCache was "
-                             "made of; make another BlockCache over the new tensors")
+        self._changeable(name)
+        super().__setattr__(name, value)
 
     def __delattr__(self, name):
-        self.__setattr__(name, None)
+        self._changeable(name)
+        super().__delattr__(name)
 
     def __reduce__(self):
         # A copy takes its own tensors' addresses.
-        return type(self), (self.k_pages, self.v_pages, self.k_scale, self.v_scale, self.k_tail, self.v_tail,
-                            self.page_table)
+        return (type(self), (*self.held, self.page_table),
+                {n: v for n, v in self.__dict__.items() if n not in self._FIXED})
 
     @classmethod
     def allocate(cls, B: int, H: int, d: int, blocks: int, *, pages: Optional[int] = None,

@@ -57,6 +57,15 @@ def test_a_shallow_copy_shares_them(cache):
     assert copy.copy(cache).args == cache.args
 
 
+def test_other_attributes_are_the_programs(cache):
+    """A default scale of the scores, and whatever a program notes on a cache."""
+    cache.softmax_scale, cache.owner = 0.5, "layer 3"
+    for twin in (copy.copy(cache), copy.deepcopy(cache), _saved(cache)):
+        assert twin.softmax_scale == 0.5 and twin.owner == "layer 3" and _addresses(twin)
+    del cache.owner
+    assert not hasattr(cache, "owner")
+
+
 @pytest.mark.gpu
 def test_calls_on_a_copy_leave_the_cache_alone():
     g = torch.Generator().manual_seed(1)
